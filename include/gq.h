@@ -375,6 +375,97 @@ gq_status gq_huffman_encode(const int32_t* d_codes, int64_t count, uint64_t* d_s
                             int64_t* d_info, void* d_ws, size_t ws_bytes, gq_stream_t stream);
 
 /*
+ * ---- running a quantized layer ----
+ *
+ * The calls below take a layer as gq_quantize_layer wrote it (b-bit codes packed LSB first,
+ * scales and zeros per row or group; w = scale (code - zero)) and multiply tokens with it.  The
+ * papers have no counterpart of them.  They cover the packed formats: uniform spacing, clip 0
+ * or 1, any order.  (The unconstrained integers of clip = 2, ZSIC's per-column steps and SSQR's
+ * outliers are not part of the packed stream.)  They need no gq_workspace_status.
+ */
+
+/*
+ * The codes of an ordered layer (gq_quantize_layer_ordered with groups) repacked in processing
+ * order, once per layer: row r of the result holds, at position k, the code of original column
+ * d_perm[k], so that a group's columns lie side by side as gq_linear and gq_linear_quantized
+ * read them (pass them the same d_perm).
+ *
+ *   d_codes   m x ceil(n*b/32) uint32, read.   d_out  the same size, written; not d_codes.
+ *   d_perm    n int32 (an entry outside 0..n-1 counts as 0; every access stays in bounds).
+ *   Limits: 1 <= m <= 2^24, 1 <= n <= 32768, 2 <= bits <= 8.
+ */
+gq_status gq_order_codes(const uint32_t* d_codes, int64_t m, int64_t n, int bits,
+                         const int32_t* d_perm, uint32_t* d_out, gq_stream_t stream);
+
+/* Workspace bytes gq_linear needs for T tokens of type x_dtype; ordered = 1 when d_perm is
+ * passed.  0: it needs none (or an argument is out of range, which the call reports). */
+size_t gq_linear_workspace_size(int64_t T, int64_t m, int64_t n, gq_dtype x_dtype, int ordered);
+
+/*
+ * y = x W^T with the packed layer W:
+ *   y[t][r] = sum over groups g of scale[r][g] * sum over k in g of x[t][k] (code[r][k] - zero[r][g]).
+ * Products of x and code - zero are exact (fp32 x as three bf16 parts that add up to it), summed
+ * in fp32 inside a group, scaled and added up in fp32; y is rounded once.  A token's result does
+ * not depend on the other tokens' values, and no sum depends on timing: equal calls give equal
+ * bits.
+ *
+ *   d_x       T x n, bf16 or fp32 (any alignment of the element type).
+ *   d_codes   m x ceil(n*b/32) uint32; d_scales m x G fp32; d_zeros m x G uint8 with values in
+ *             [0, 2^b - 1], G = 1 (group_size 0) or ceil(n / group_size).
+ *   bits      2..8.   group_size  0, 16, 32, 64 or 128.
+ *   d_perm    NULL, or n int32: column k of the codes multiplies x[:, d_perm[k]] (a layer of
+ *             gq_order_codes).  An ordered layer with group_size 0 keeps its original columns
+ *             and needs no d_perm.  Entries outside 0..n-1 count as 0.
+ *   d_y       T x m, bf16 or fp32, written; must not overlap an input.
+ *   d_ws      workspace of at least gq_linear_workspace_size(T, m, n, x_dtype, ordered) bytes
+ *             (may be NULL when that is 0).
+ * Limits: 0 <= T < 2^31 (T = 0 does nothing), 1 <= m <= 2^24, 1 <= n <= 32768.
+ */
+gq_status gq_linear(const void* d_x, gq_dtype x_dtype, int64_t T, int64_t m, int64_t n,
+                    const uint32_t* d_codes, const float* d_scales, const uint8_t* d_zeros,
+                    int bits, int group_size, const int32_t* d_perm, void* d_y, gq_dtype y_dtype,
+                    void* d_ws, size_t ws_bytes, gq_stream_t stream);
+
+/* Workspace bytes gq_linear_quantized needs for T tokens, as gq_linear_workspace_size. */
+size_t gq_linear_quantized_workspace_size(int64_t T, int64_t m, int64_t n, int ordered);
+
+/*
+ * gq_linear on 8-bit rows (gq_rmsnorm_quantize): x[t][k] = d_qscale[t] * d_q[t][k].  The sums of
+ * one group are integers; d_qscale multiplies the finished sum.
+ *
+ *   d_q       T x n int8.   d_qscale  T fp32.   Everything else as gq_linear.
+ */
+gq_status gq_linear_quantized(const int8_t* d_q, const float* d_qscale, int64_t T, int64_t m,
+                              int64_t n, const uint32_t* d_codes, const float* d_scales,
+                              const uint8_t* d_zeros, int bits, int group_size,
+                              const int32_t* d_perm, void* d_y, gq_dtype y_dtype, void* d_ws,
+                              size_t ws_bytes, gq_stream_t stream);
+
+/*
+ * Root-mean-square norm of T rows with the residual's addition, and the normalised rows in 8
+ * bits for gq_linear_quantized:
+ *   h = x + residual, rounded to x_dtype and stored in d_sum,
+ *   rstd = 1 / sqrt(mean(h^2) + eps),   d_y = h gamma rstd,
+ *   d_q = rint(127 u / max|u|) with u = h gamma (half to even; 0 in a row of zeros),
+ *   d_qscale = max|u| rstd / 127, so that d_qscale d_q stands for h gamma rstd.
+ * Statistics and the decision of every code are in fp64.  A row with an infinity or a NaN in it
+ * gets the scale NaN and codes 0; other rows are not affected.
+ *
+ *   d_x         T x n, bf16 or fp32.   d_residual  T x n of the same type, or NULL (h = x).
+ *   d_gamma     n, bf16 or fp32 (gamma_dtype).   eps >= 0, finite.
+ *   d_sum       T x n of x_dtype, or NULL (not stored).  May be d_x or d_residual themselves.
+ *   d_y         T x n of x_dtype, or NULL (not written).  May be d_x or d_residual themselves
+ *               unless d_sum is the same array.
+ *   d_q         T x n int8 with d_qscale (T fp32), or both NULL.  One of d_y and d_q is needed.
+ *   Other overlaps of outputs and inputs are not allowed.
+ * Limits: 0 <= T < 2^31 (T = 0 does nothing), 1 <= n <= 32768.
+ */
+gq_status gq_rmsnorm_quantize(const void* d_x, const void* d_residual, gq_dtype x_dtype,
+                              const void* d_gamma, gq_dtype gamma_dtype, int64_t T, int64_t n,
+                              double eps, void* d_sum, void* d_y, int8_t* d_q, float* d_qscale,
+                              gq_stream_t stream);
+
+/*
  * Test setting of the bounded device waits, for tests of the timeout path (process-wide, read
  * when a call is enqueued; default off).  poll_limit > 0 replaces the poll budget of the
  * factor's per-pivot waits in gq_prepare_hinv(_ordered) (0 restores the default of about 2^26

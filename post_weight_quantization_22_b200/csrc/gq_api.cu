@@ -26,6 +26,7 @@ namespace {
 
 constexpr int64_t kMaxN = 32768;
 constexpr int64_t kMaxM = int64_t(1) << 24;
+constexpr int64_t kMaxT = (int64_t(1) << 31) - 1;  // tokens of the running calls
 
 std::mutex g_init_mu;
 bool g_init_done[128] = {};
@@ -45,6 +46,9 @@ gq_status ensure_device_setup() {
 }
 
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+bool aligned_to(const void* p, uintptr_t bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0;
+}
 
 // ---- launch-sequence graphs -------------------------------------------------------------
 // A call's kernel sequence (hundreds of small dependent launches for the factorisation) is
@@ -363,6 +367,97 @@ gq_status gq_hptq_quantize_layer(const void* d_W, gq_dtype w_dtype, int64_t m, i
   o.budget = budget; o.steps = steps; o.max_doublings = max_doublings; o.alpha = d_alpha;
   o.total_bits = reinterpret_cast<long long*>(d_total_bits);
   return run_hptq(a, o, (cudaStream_t)stream);  // synchronizes once per pass
+}
+
+gq_status gq_order_codes(const uint32_t* d_codes, int64_t m, int64_t n, int bits,
+                         const int32_t* d_perm, uint32_t* d_out, gq_stream_t stream) {
+  if (m < 1 || m > kMaxM || n < 1 || n > kMaxN || bits < 2 || bits > 8) return GQ_ERR_INVALID_ARG;
+  if (!d_codes || !d_perm || !d_out || d_codes == d_out) return GQ_ERR_INVALID_ARG;
+  if (!aligned_to(d_codes, 4) || !aligned_to(d_perm, 4) || !aligned_to(d_out, 4))
+    return GQ_ERR_INVALID_ARG;
+  return launch_order_codes(d_codes, m, n, bits, d_perm, d_out, (cudaStream_t)stream) ==
+                 cudaSuccess
+             ? GQ_OK : GQ_ERR_CUDA;
+}
+
+static size_t linear_ws(int64_t T, int64_t m, int64_t n, int kind, int ordered) {
+  if (T < 0 || T > kMaxT || m < 1 || m > kMaxM || n < 1 || n > kMaxN) return 0;
+  if (ordered != 0 && ordered != 1) return 0;
+  if (kind != kXBf16 && kind != kXFp32 && kind != kXInt8) return 0;
+  return 0;
+}
+
+size_t gq_linear_workspace_size(int64_t T, int64_t m, int64_t n, gq_dtype x_dtype, int ordered) {
+  if (x_dtype != GQ_BF16 && x_dtype != GQ_FP32) return 0;
+  return linear_ws(T, m, n, x_dtype == GQ_BF16 ? kXBf16 : kXFp32, ordered);
+}
+
+size_t gq_linear_quantized_workspace_size(int64_t T, int64_t m, int64_t n, int ordered) {
+  return linear_ws(T, m, n, kXInt8, ordered);
+}
+
+static gq_status linear_common(const LinearArgs& a, LinearInput kind, gq_dtype y_dtype, void* d_ws,
+                               size_t ws_bytes, gq_stream_t stream) {
+  if (a.T < 0 || a.T > kMaxT || a.m < 1 || a.m > kMaxM || a.n < 1 || a.n > kMaxN)
+    return GQ_ERR_INVALID_ARG;
+  if (y_dtype != GQ_BF16 && y_dtype != GQ_FP32) return GQ_ERR_INVALID_ARG;
+  if (a.bits < 2 || a.bits > 8) return GQ_ERR_INVALID_ARG;
+  const int g = a.group;
+  if (g != 0 && g != 16 && g != 32 && g != 64 && g != 128)
+    return (g > 0 && g <= 128 && kBlock % g == 0) ? GQ_ERR_UNSUPPORTED : GQ_ERR_INVALID_ARG;
+  if (a.T == 0) return GQ_OK;
+  if (!a.x || !a.codes || !a.scales || !a.zeros || !a.y) return GQ_ERR_INVALID_ARG;
+  if (kind == kXInt8 && !a.xscale) return GQ_ERR_INVALID_ARG;
+  if (!aligned_to(a.x, kind == kXInt8 ? 1 : kind == kXBf16 ? 2 : 4) || !aligned_to(a.codes, 4) ||
+      !aligned_to(a.scales, 4) || !aligned_to(a.perm, 4) || !aligned_to(a.xscale, 4) ||
+      !aligned_to(a.y, y_dtype == GQ_BF16 ? 2 : 4))
+    return GQ_ERR_INVALID_ARG;
+  const size_t need = linear_ws(a.T, a.m, a.n, kind, a.perm != nullptr);
+  if (need > 0 && (!d_ws || !aligned256(d_ws) || ws_bytes < need)) return GQ_ERR_WORKSPACE;
+  gq_status st = ensure_device_setup();
+  if (st != GQ_OK) return st;
+  return launch_linear_rows(a, kind, (cudaStream_t)stream) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+}
+
+gq_status gq_linear(const void* d_x, gq_dtype x_dtype, int64_t T, int64_t m, int64_t n,
+                    const uint32_t* d_codes, const float* d_scales, const uint8_t* d_zeros,
+                    int bits, int group_size, const int32_t* d_perm, void* d_y, gq_dtype y_dtype,
+                    void* d_ws, size_t ws_bytes, gq_stream_t stream) {
+  if (x_dtype != GQ_BF16 && x_dtype != GQ_FP32) return GQ_ERR_INVALID_ARG;
+  const LinearArgs a{d_x, nullptr, T, m, n, d_codes, d_scales, d_zeros, bits, group_size, d_perm,
+                     d_y, y_dtype == GQ_BF16};
+  return linear_common(a, x_dtype == GQ_BF16 ? kXBf16 : kXFp32, y_dtype, d_ws, ws_bytes, stream);
+}
+
+gq_status gq_linear_quantized(const int8_t* d_q, const float* d_qscale, int64_t T, int64_t m,
+                              int64_t n, const uint32_t* d_codes, const float* d_scales,
+                              const uint8_t* d_zeros, int bits, int group_size,
+                              const int32_t* d_perm, void* d_y, gq_dtype y_dtype, void* d_ws,
+                              size_t ws_bytes, gq_stream_t stream) {
+  const LinearArgs a{d_q, d_qscale, T, m, n, d_codes, d_scales, d_zeros, bits, group_size, d_perm,
+                     d_y, y_dtype == GQ_BF16};
+  return linear_common(a, kXInt8, y_dtype, d_ws, ws_bytes, stream);
+}
+
+gq_status gq_rmsnorm_quantize(const void* d_x, const void* d_residual, gq_dtype x_dtype,
+                              const void* d_gamma, gq_dtype gamma_dtype, int64_t T, int64_t n,
+                              double eps, void* d_sum, void* d_y, int8_t* d_q, float* d_qscale,
+                              gq_stream_t stream) {
+  if (x_dtype != GQ_BF16 && x_dtype != GQ_FP32) return GQ_ERR_INVALID_ARG;
+  if (gamma_dtype != GQ_BF16 && gamma_dtype != GQ_FP32) return GQ_ERR_INVALID_ARG;
+  if (T < 0 || T > kMaxT || n < 1 || n > kMaxN) return GQ_ERR_INVALID_ARG;
+  if (!(eps >= 0.0 && eps <= 1e300)) return GQ_ERR_INVALID_ARG;
+  if (T == 0) return GQ_OK;
+  if (!d_x || !d_gamma || (!d_y && !d_q) || (!d_q != !d_qscale)) return GQ_ERR_INVALID_ARG;
+  if (d_sum && d_sum == d_y) return GQ_ERR_INVALID_ARG;
+  const uintptr_t xa = x_dtype == GQ_BF16 ? 2 : 4;
+  if (!aligned_to(d_x, xa) || !aligned_to(d_residual, xa) || !aligned_to(d_sum, xa) ||
+      !aligned_to(d_y, xa) || !aligned_to(d_gamma, gamma_dtype == GQ_BF16 ? 2 : 4) ||
+      !aligned_to(d_qscale, 4))
+    return GQ_ERR_INVALID_ARG;
+  const NormArgs a{d_x, d_residual, d_gamma, T, n, eps, d_sum, d_y, d_q, d_qscale};
+  return launch_rmsnorm(a, x_dtype, gamma_dtype, (cudaStream_t)stream) == cudaSuccess
+             ? GQ_OK : GQ_ERR_CUDA;
 }
 
 gq_status gq_zsic_spacing(const float* d_U, int64_t n, double* d_kappa, gq_stream_t stream) {

@@ -214,4 +214,38 @@ cudaError_t launch_lazy_tc(const LazyTcMaps& maps, float* Wf, int64_t n, int64_t
                            int64_t k0, int K, int64_t j1, int64_t jend, WsHeader* hdr,
                            cudaStream_t s);
 
+// ---- products with a packed layer (gq_linear.cu) ----
+enum LinearInput { kXBf16 = 0, kXFp32 = 1, kXInt8 = 2 };
+struct LinearArgs {
+  const void* x;         // T x n: bf16, fp32 or int8 (a LinearInput)
+  const float* xscale;   // T (int8 rows only)
+  int64_t T, m, n;
+  const uint32_t* codes;
+  const float* scales;   // m x G
+  const uint8_t* zeros;  // m x G
+  int bits, group;
+  const int32_t* perm;   // column k of the codes multiplies x[:, perm[k]] (null: k)
+  void* y;               // T x m
+  int y_bf16;            // output type: 1 bf16, 0 fp32
+};
+// The product on the warp-level tensor cores, for few tokens (correct for any T).
+cudaError_t launch_linear_rows(const LinearArgs& a, LinearInput kind, cudaStream_t s);
+cudaError_t launch_order_codes(const uint32_t* codes, int64_t m, int64_t n, int bits,
+                               const int32_t* perm, uint32_t* out, cudaStream_t s);
+
+// ---- root-mean-square norm with 8-bit rows (gq_norm.cu) ----
+struct NormArgs {
+  const void* x;
+  const void* residual;  // null: none
+  const void* gamma;
+  int64_t T, n;
+  double eps;
+  void* sum;             // null: not stored
+  void* y;               // null: not written
+  int8_t* q;             // null: not written
+  float* qscale;
+};
+cudaError_t launch_rmsnorm(const NormArgs& a, gq_dtype x_dtype, gq_dtype gamma_dtype,
+                           cudaStream_t s);
+
 }  // namespace gq

@@ -80,6 +80,19 @@ def _load():
                                            P, P, P, P, P, SZ, P]
     lib.gq_zsic_spacing.restype = I
     lib.gq_zsic_spacing.argtypes = [P, I64, P, P]
+    D = ctypes.c_double
+    lib.gq_order_codes.restype = I
+    lib.gq_order_codes.argtypes = [P, I64, I64, I, P, P, P]
+    lib.gq_linear_workspace_size.restype = SZ
+    lib.gq_linear_workspace_size.argtypes = [I64, I64, I64, I, I]
+    lib.gq_linear.restype = I
+    lib.gq_linear.argtypes = [P, I, I64, I64, I64, P, P, P, I, I, P, P, I, P, SZ, P]
+    lib.gq_linear_quantized_workspace_size.restype = SZ
+    lib.gq_linear_quantized_workspace_size.argtypes = [I64, I64, I64, I]
+    lib.gq_linear_quantized.restype = I
+    lib.gq_linear_quantized.argtypes = [P, P, I64, I64, I64, P, P, P, I, I, P, P, I, P, SZ, P]
+    lib.gq_rmsnorm_quantize.restype = I
+    lib.gq_rmsnorm_quantize.argtypes = [P, P, I, P, I, I64, I64, D, P, P, P, P, P]
     lib.gq_debug_wait_test.restype = I
     lib.gq_debug_wait_test.argtypes = [ctypes.c_uint32, I]
     lib.gq_workspace_status.restype = I
@@ -95,7 +108,8 @@ EXPORTED = ("gq_version", "gq_status_string", "gq_hessian_accumulate", "gq_hessi
             "gq_quantize_layer_ordered", "gq_zsic_spacing", "gq_huffman_workspace_size",
             "gq_huffman_encode", "gq_debug_wait_test", "gq_kernel_launches",
             "gq_ssqr_workspace_size", "gq_ssqr_quantize_layer", "gq_hptq_workspace_size",
-            "gq_hptq_quantize_layer")
+            "gq_hptq_quantize_layer", "gq_order_codes", "gq_linear_workspace_size", "gq_linear",
+            "gq_linear_quantized_workspace_size", "gq_linear_quantized", "gq_rmsnorm_quantize")
 
 
 def _ptr(t):
@@ -404,6 +418,174 @@ def gq_huffman_encode(codes: torch.Tensor, stream_words: int | None = None, ws=N
                                  _ptr(cw), _ptr(info), _ptr(ws), ws.numel(), _stream(stream)),
            "gq_huffman_encode")
     return out, lengths, cw, info, ws
+
+
+# ---------------------------------------------------------------------------------------------
+# running a quantized layer
+# ---------------------------------------------------------------------------------------------
+# These calls run on the tensors' device, whichever is current, and on ``stream`` (default: that
+# device's current stream); what they allocate is allocated on that stream.
+
+class _On:
+    """The tensors' device and the call's stream made current (only where they are not)."""
+
+    def __init__(self, dev, stream):
+        self.ctx = []
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+            self.ctx.append(torch.cuda.stream(stream))
+        elif dev.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(dev))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def _need_on(t, dtype, shape, dev, name):
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dev} {dtype} {tuple(shape)}, got "
+                         f"{t.device} {t.dtype} {tuple(t.shape)}")
+
+
+def _rows(x, name):
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous cuda matrix (tokens x features), got "
+                         f"{x.device} {tuple(x.shape)}")
+    return x.shape
+
+
+def _layer_args(codes, scales, zeros, n, bits, group_size, perm, dev):
+    if not 2 <= bits <= 8:
+        raise ValueError(f"bits: 2 to 8, got {bits}")
+    if codes.dim() != 2:
+        raise ValueError("codes: expected rows of packed words")
+    m = codes.shape[0]
+    G = 1 if group_size == 0 else -(-n // group_size)
+    _need_on(codes, torch.int32, (m, (n * bits + 31) // 32), dev, "codes")
+    _need_on(scales, torch.float32, (m, G), dev, "scales")
+    _need_on(zeros, torch.uint8, (m, G), dev, "zeros")
+    if perm is not None:
+        _need_on(perm, torch.int32, (n,), dev, "perm")
+    return m
+
+
+def gq_order_codes(codes: torch.Tensor, n: int, bits: int, perm: torch.Tensor, out=None,
+                   stream=None) -> torch.Tensor:
+    """The packed codes of an ordered layer (m x words, columns as in W) with the columns in
+    processing order: once per layer, for gq_linear / gq_linear_quantized with the same perm."""
+    if not 2 <= bits <= 8:
+        raise ValueError(f"bits: 2 to 8, got {bits}")
+    m, _ = _rows(codes, "codes")
+    dev = codes.device
+    _need_on(codes, torch.int32, (m, n_words(n, bits)), dev, "codes")
+    _need_on(perm, torch.int32, (n,), dev, "perm")
+    with _On(dev, stream):
+        out = torch.empty_like(codes) if out is None else out
+        _need_on(out, torch.int32, codes.shape, dev, "out")
+        _check(LIB.gq_order_codes(codes.data_ptr(), m, n, bits, perm.data_ptr(), out.data_ptr(),
+                                  torch.cuda.current_stream(dev).cuda_stream), "gq_order_codes")
+    return out
+
+
+def gq_linear_workspace_size(T: int, m: int, n: int, x_dtype=torch.bfloat16,
+                             ordered: bool = False) -> int:
+    if x_dtype == torch.int8:
+        return int(LIB.gq_linear_quantized_workspace_size(T, m, n, int(bool(ordered))))
+    code = GQ_BF16 if x_dtype == torch.bfloat16 else GQ_FP32
+    return int(LIB.gq_linear_workspace_size(T, m, n, code, int(bool(ordered))))
+
+
+def gq_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+              bits: int, group_size: int = 0, perm=None, y=None, y_dtype=None, ws=None,
+              stream=None) -> torch.Tensor:
+    """y = x W^T (T x m) with a packed layer (gq_quantize_layer); x T x n in bf16 or fp32, y in
+    ``y_dtype`` (default: x's).  ``perm``: the codes are in processing order (gq_order_codes)."""
+    T, n = _rows(x, "x")
+    dev = x.device
+    xc = _dtype_code(x)
+    m = _layer_args(codes, scales, zeros, n, bits, group_size, perm, dev)
+    with _On(dev, stream):
+        if y is None:
+            y = torch.empty((T, m), dtype=x.dtype if y_dtype is None else y_dtype, device=dev)
+        yc = _dtype_code(y)
+        _need_on(y, y.dtype, (T, m), dev, "y")
+        if ws is None:
+            need = LIB.gq_linear_workspace_size(T, m, n, xc, int(perm is not None))
+            ws = workspace(need, dev) if need else None
+        _check(LIB.gq_linear(x.data_ptr(), xc, T, m, n, codes.data_ptr(), scales.data_ptr(),
+                             zeros.data_ptr(), bits, group_size,
+                             None if perm is None else perm.data_ptr(), y.data_ptr(), yc,
+                             None if ws is None else ws.data_ptr(),
+                             0 if ws is None else ws.numel(),
+                             torch.cuda.current_stream(dev).cuda_stream), "gq_linear")
+    return y
+
+
+def gq_linear_quantized(q: torch.Tensor, qscale: torch.Tensor, codes: torch.Tensor,
+                        scales: torch.Tensor, zeros: torch.Tensor, bits: int,
+                        group_size: int = 0, perm=None, y=None, y_dtype=torch.bfloat16, ws=None,
+                        stream=None) -> torch.Tensor:
+    """gq_linear on 8-bit rows: x = qscale[:, None] * q (q int8 T x n, qscale fp32 T)."""
+    T, n = _rows(q, "q")
+    dev = q.device
+    _need_on(q, torch.int8, (T, n), dev, "q")
+    _need_on(qscale, torch.float32, (T,), dev, "qscale")
+    m = _layer_args(codes, scales, zeros, n, bits, group_size, perm, dev)
+    with _On(dev, stream):
+        if y is None:
+            y = torch.empty((T, m), dtype=y_dtype, device=dev)
+        yc = _dtype_code(y)
+        _need_on(y, y.dtype, (T, m), dev, "y")
+        if ws is None:
+            need = LIB.gq_linear_quantized_workspace_size(T, m, n, int(perm is not None))
+            ws = workspace(need, dev) if need else None
+        _check(LIB.gq_linear_quantized(
+            q.data_ptr(), qscale.data_ptr(), T, m, n, codes.data_ptr(), scales.data_ptr(),
+            zeros.data_ptr(), bits, group_size, None if perm is None else perm.data_ptr(),
+            y.data_ptr(), yc, None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel(),
+            torch.cuda.current_stream(dev).cuda_stream), "gq_linear_quantized")
+    return y
+
+
+def gq_rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residual=None,
+                        sum=None, y=None, q=None, qscale=None, stream=None) -> dict:
+    """h = x + residual, v = h / sqrt(mean(h^2) + eps) * gamma; v as y (x's type) and / or as 8-bit
+    rows q with qscale.  ``sum`` (h) is stored with a residual, or where a tensor is given; y only
+    where a tensor is given; q unless y alone is given.  Returns dict(sum, y, q, qscale), None
+    where not written."""
+    T, n = _rows(x, "x")
+    dev = x.device
+    xc, gc = _dtype_code(x), _dtype_code(gamma)
+    _need_on(gamma, gamma.dtype, (n,), dev, "gamma")
+    if (q is None) != (qscale is None):
+        raise ValueError("q and qscale go together")
+    with _On(dev, stream):
+        if residual is not None:
+            _need_on(residual, x.dtype, (T, n), dev, "residual")
+            sum = torch.empty_like(x) if sum is None else sum
+        if q is None and y is None:
+            q = torch.empty((T, n), dtype=torch.int8, device=dev)
+            qscale = torch.empty(T, dtype=torch.float32, device=dev)
+        if sum is not None:
+            _need_on(sum, x.dtype, (T, n), dev, "sum")
+        if y is not None:
+            _need_on(y, x.dtype, (T, n), dev, "y")
+        if q is not None:
+            _need_on(q, torch.int8, (T, n), dev, "q")
+            _need_on(qscale, torch.float32, (T,), dev, "qscale")
+        ptr = [None if t is None else t.data_ptr() for t in (residual, sum, y, q, qscale)]
+        _check(LIB.gq_rmsnorm_quantize(x.data_ptr(), ptr[0], xc, gamma.data_ptr(), gc, T, n,
+                                       eps, ptr[1], ptr[2], ptr[3], ptr[4],
+                                       torch.cuda.current_stream(dev).cuda_stream),
+               "gq_rmsnorm_quantize")
+    return dict(sum=sum, y=y, q=q, qscale=qscale)
 
 
 def gq_debug_wait_test(poll_limit: int = 0, withhold_arrival: bool = False) -> None:
