@@ -41,6 +41,7 @@ gq_status ensure_device_setup() {
   if (lazy_tc_init_attributes() != cudaSuccess) return GQ_ERR_CUDA;
   if (hessian_init_attributes() != cudaSuccess) return GQ_ERR_CUDA;
   if (huffman_init_attributes() != cudaSuccess) return GQ_ERR_CUDA;
+  if (linear_init_attributes() != cudaSuccess) return GQ_ERR_CUDA;
   g_init_done[dev] = true;
   return GQ_OK;
 }
@@ -384,7 +385,7 @@ static size_t linear_ws(int64_t T, int64_t m, int64_t n, int kind, int ordered) 
   if (T < 0 || T > kMaxT || m < 1 || m > kMaxM || n < 1 || n > kMaxN) return 0;
   if (ordered != 0 && ordered != 1) return 0;
   if (kind != kXBf16 && kind != kXFp32 && kind != kXInt8) return 0;
-  return 0;
+  return linear_ws_bytes(T, n, (LinearInput)kind, ordered != 0);
 }
 
 size_t gq_linear_workspace_size(int64_t T, int64_t m, int64_t n, gq_dtype x_dtype, int ordered) {
@@ -416,7 +417,7 @@ static gq_status linear_common(const LinearArgs& a, LinearInput kind, gq_dtype y
   if (need > 0 && (!d_ws || !aligned256(d_ws) || ws_bytes < need)) return GQ_ERR_WORKSPACE;
   gq_status st = ensure_device_setup();
   if (st != GQ_OK) return st;
-  return launch_linear_rows(a, kind, (cudaStream_t)stream) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+  return launch_linear(a, kind, d_ws, (cudaStream_t)stream) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
 }
 
 gq_status gq_linear(const void* d_x, gq_dtype x_dtype, int64_t T, int64_t m, int64_t n,

@@ -62,14 +62,6 @@ __device__ __forceinline__ void load_codes(const uint32_t* __restrict__ row, int
   }
 }
 
-// Three bf16 parts of an fp32 value, by truncation: their sum is the value (8 + 8 + 8 bits).
-__device__ __forceinline__ void split3(float v, uint32_t& h, uint32_t& mid, uint32_t& low) {
-  h = __float_as_uint(v) & 0xFFFF0000u;
-  const float r = fabsf(v) == __int_as_float(0x7F800000) ? 0.f : v - __uint_as_float(h);
-  mid = __float_as_uint(r) & 0xFFFF0000u;
-  low = __float_as_uint(r - __uint_as_float(mid));
-}
-
 // The lane's eight inputs x[k .. k+7] of one token as pairs (i, i + 4), P parts each.
 template <LinearInput K, int P>
 __device__ __forceinline__ void load_x(const void* xrow, int64_t k, int64_t n,

@@ -1,0 +1,548 @@
+// Products with a packed layer for many tokens, on the 5th-generation tensor cores.
+//
+// y[t][r] = sum_g s[r][g] sum_{k in g} x[t][k] (c[r][k] - z[r][g]).  A CTA computes 128 rows x N
+// tokens: the rows' codes are unpacked into bf16 tiles (c - z is an integer of at most 8 bits and
+// a sign: exact) that are the instruction's A operand, the tokens come by TMA as its B operand,
+// and every group's sum is formed in a tensor-memory accumulator of its own, two in turn.  Eight
+// warps take a finished accumulator out, multiply it with the group's scale in fp32 (a thread
+// holds one row, so the scale is one register) and add it to sums in registers while the next
+// group is multiplied.  No weight is rounded, and no chain of tensor-core additions is longer
+// than 256 columns.
+//
+// Roles: warp 0 the tokens' TMA loads, warp 1 the MMAs, warps 4-7 unpack, warps 8-15 scale and
+// add.  With fewer tiles than SMs a cluster shares one tile's columns, and its CTAs add their
+// sums over distributed shared memory in a fixed order.
+#include "gq_internal.cuh"
+#include "gq_tc.cuh"
+#include "gq_unpack.cuh"
+
+namespace gq {
+
+namespace {
+constexpr int kLinThreads = 512;
+constexpr int kChunk = 128;                       // columns per A slot
+constexpr uint32_t kASub = 128 * 64 * 2;          // 64 columns of 128 rows
+constexpr uint32_t kASlot = 2 * kASub;
+constexpr int kASlots = 2;
+constexpr uint32_t kBRing = 128 * 1024;
+constexpr size_t kLinSmem = kASlots * kASlot + kBRing + 1024 + 512;
+
+struct LinTcArgs {
+  LinearArgs l;
+  int planes_t;      // rows between two parts of the tokens (0 with one part)
+  int N;             // tokens per tile
+  int mtiles, ntiles;
+  int chunks;        // chunks of 128 columns
+  WsHeader* hdr;
+};
+
+// Waits as mbar_wait, but also gives up when another role of the CTA has.
+__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  for (uint32_t i = 0; i < tc::kDefaultPolls; ++i) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023) == 1023 && *fail) return false;
+  }
+  *fail = 1;
+  return false;
+}
+
+__device__ __forceinline__ void fma2(uint64_t& acc, float a, float b, uint64_t s) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t local, uint32_t rank) {
+  uint32_t remote;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+// The B words of one unit of 32 columns (words behind the row's end are 0).  vec: rows and base
+// allow the widest loads that a unit's size allows.
+template <int B>
+__device__ __forceinline__ void load_unit(const uint32_t* __restrict__ row, int unit, int words,
+                                          bool vec, uint32_t (&w)[B]) {
+  const int w0 = unit * B;
+  if (vec && w0 + B <= words) {
+    if constexpr (B % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < B / 4; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + w0) + i);
+        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+      }
+      return;
+    } else if constexpr (B % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < B / 2; ++i) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + w0) + i);
+        w[2 * i] = v.x; w[2 * i + 1] = v.y;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < B; ++i) w[i] = w0 + i < words ? __ldg(row + w0 + i) : 0u;
+}
+}  // namespace
+
+// kN: the largest N; P: parts of the tokens (3 for fp32).
+template <int B, int P, int kN>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    linear_tc_kernel(const __grid_constant__ CUtensorMap m_x, LinTcArgs a, int vec) {
+  constexpr uint32_t kBSlot = kN * 128;
+  constexpr int kBSlots = (int)(kBRing / kBSlot);
+  static_assert(kBSlots >= P + 1, "the parts of one step have to fit the ring");
+  extern __shared__ uint8_t lin_smem[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(lin_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t* bring = base + kASlots * kASlot;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(bring + kBRing);
+  uint64_t* a_full = bars;
+  uint64_t* a_empty = a_full + kASlots;
+  uint64_t* b_full = a_empty + kASlots;
+  uint64_t* b_empty = b_full + kBSlots;
+  uint64_t* t_full = b_empty + kBSlots;
+  uint64_t* t_empty = t_full + 2;
+  uint64_t* done = t_empty + 2;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* fail = reinterpret_cast<volatile int*>(tslot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t S = cluster_size(), rank = cluster_rank();
+  const unsigned tile = blockIdx.x / S;
+  const int mt = (int)(tile % (unsigned)a.mtiles);
+  const int64_t row0 = (int64_t)mt * 128;
+  const int64_t t0 = (int64_t)(tile / (unsigned)a.mtiles) * a.N;
+  const int N = a.N;
+  // this CTA's chunks; pairs of chunks stay together (a period may span two)
+  const int pairs = (a.chunks + 1) / 2;
+  const int c0 = 2 * (int)((int64_t)pairs * rank / S);
+  const int c1 = min(a.chunks, 2 * (int)((int64_t)pairs * (rank + 1) / S));
+  const int gs = a.l.group;
+  const int dk = gs ? gs / 16 : 16;               // 16-column steps per accumulator period
+  const int steps = (c1 - c0) * 8;
+  const int periods = (steps + dk - 1) / dk;
+
+  if (blockIdx.x == 0 && tid == 0) a.hdr->status = 0;  // no wait can run out for a second yet
+  if (tid == 0) {
+    for (int i = 0; i < kASlots; ++i) { tc::mbar_init(&a_full[i], 128); tc::mbar_init(&a_empty[i], 1); }
+    for (int i = 0; i < kBSlots; ++i) { tc::mbar_init(&b_full[i], 1); tc::mbar_init(&b_empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { tc::mbar_init(&t_full[i], 1); tc::mbar_init(&t_empty[i], 256); }
+    tc::mbar_init(done, 1);
+    *fail = 0;
+    tc::fence_barrier_init();
+    tc::prefetch_tmap(&m_x);
+  }
+  if (warp == 2) tc::tmem_alloc(tslot, 2 * kN);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tslot;
+
+  if (warp < 4) {
+    if constexpr (kN > 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0 && lane == 0) {
+      // tokens: 64 columns of every part per step of the ring
+      int i = 0;
+      const int subs = (c1 - c0) * 2;
+      bool ok = true;
+      for (int sub = 0; sub < subs && ok; ++sub) {
+#pragma unroll
+        for (int p = 0; p < P; ++p, ++i) {
+          const int s = i % kBSlots;
+          if (i >= kBSlots && !wait_or_fail(&b_empty[s], ((i / kBSlots) - 1) & 1, fail)) {
+            ok = false;
+            break;
+          }
+          tc::mbar_arrive_expect_tx(&b_full[s], (uint32_t)N * 128);
+          tc::tma_load_2d(bring + s * kBSlot, &m_x, &b_full[s], c0 * kChunk + sub * 64,
+                          (int)(t0 + (int64_t)p * a.planes_t));
+        }
+      }
+      if (!ok)  // no copy may be in flight when the CTA ends
+        for (int j = max(0, i - kBSlots); j < i; ++j)
+          tc::mbar_wait(&b_full[j % kBSlots], (j / kBSlots) & 1);
+    } else if (warp == 1 && lane == 0) {
+      const uint32_t idesc = tc::idesc_f32acc(1, 1, 0, 0, 128, (uint32_t)N);
+      int i = 0, step = 0, period = 0;
+      bool ok = true;
+      for (int c = 0; c < c1 - c0 && ok; ++c) {
+        const int sa = c % kASlots;
+        if (!wait_or_fail(&a_full[sa], (c / kASlots) & 1, fail)) break;
+        for (int sub = 0; sub < 2 && ok; ++sub) {
+          for (int p = 0; p < P; ++p)
+            ok = ok && wait_or_fail(&b_full[(i + p) % kBSlots], ((i + p) / kBSlots) & 1, fail);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t at = tc::smem_u32(base + sa * kASlot + sub * kASub);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int buf = period & 1;
+            const bool first = step % dk == 0;
+            if (first && period >= 2) {
+              ok = ok && wait_or_fail(&t_empty[buf], ((period >> 1) - 1) & 1, fail);
+              tc::fence_after_sync();
+            }
+            if (ok) {
+              const uint64_t da = tc::sdesc(at + k * 32, 16, 1024, tc::kLayoutSW128);
+              for (int p = 0; p < P; ++p) {
+                const uint32_t bt = tc::smem_u32(bring + ((i + p) % kBSlots) * kBSlot);
+                const uint64_t db = tc::sdesc(bt + k * 32, 16, 1024, tc::kLayoutSW128);
+                tc::mma_f16(tmem + buf * kN, da, db, idesc, !(first && p == 0));
+              }
+            }
+            ++step;
+            if (ok && (step % dk == 0 || step == steps)) {
+              tc::mma_commit(&t_full[buf]);
+              ++period;
+            }
+          }
+          for (int p = 0; p < P; ++p, ++i) tc::mma_commit(&b_empty[i % kBSlots]);
+        }
+        tc::mma_commit(&a_empty[sa]);
+      }
+      tc::mma_commit(done);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    if constexpr (kN > 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    // unpack: a thread takes one unit of 32 columns of rows 8 i + lane % 8, i = 0..3, of its
+    // warp's 32 rows (a warp reads 8 rows x 16 b bytes at a time; its 16-byte stores of one
+    // column block fall on 8 different rows, so the swizzled tile takes them without conflicts)
+    const int words = (int)row_words(a.l.n, B);
+    const int G = gs ? (int)((a.l.n + gs - 1) / gs) : 1;
+    const int u4 = lane >> 3;
+    const uint32_t* rp[4];
+    const uint8_t* zp[4];
+    uint32_t w[4][B], z[4][2];
+    const int r_in = (warp - 4) * 32 + (lane & 7);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = min(row0 + r_in + 8 * i, a.l.m - 1);
+      rp[i] = a.l.codes + r * words;
+      zp[i] = a.l.zeros + r * G;
+    }
+    auto load = [&](int c) {
+      const int unit = (c0 + c) * 4 + u4;
+      const int g0 = gs ? min(unit * 32 / gs, G - 1) : 0;
+      const int g1 = gs == 16 ? min(unit * 2 + 1, G - 1) : g0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        load_unit<B>(rp[i], unit, words, vec, w[i]);
+        z[i][0] = __ldg(zp[i] + g0);
+        z[i][1] = gs == 16 ? __ldg(zp[i] + g1) : z[i][0];
+      }
+    };
+    if (c1 > c0) load(0);
+    for (int c = 0; c < c1 - c0; ++c) {
+      const int sa = c % kASlots;
+      if (c >= kASlots && !wait_or_fail(&a_empty[sa], ((c / kASlots) - 1) & 1, fail)) break;
+      uint8_t* tilep = base + sa * kASlot + (u4 >> 1) * kASub;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r_in + 8 * i;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // eight columns
+          constexpr int kTop = B - 1;
+          const int q = (j * B) / 4, sh = 8 * ((j * B) % 4);
+          const uint32_t w0 = w[i][q], w1 = w[i][q + 1 < B ? q + 1 : kTop];
+          const uint32_t w2 = w[i][q + 2 < B ? q + 2 : kTop];
+          uint32_t pr[4];
+          code_pairs<B>(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh), pr);
+          const uint32_t zz = zero_pair<B, false>(z[i][j >> 1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pr[e] = pair_value<B, false>(pr[e], zz);
+          uint4 v;  // from pairs (e, e + 4) to columns in order
+          v.x = __byte_perm(pr[0], pr[1], 0x5410);
+          v.y = __byte_perm(pr[2], pr[3], 0x5410);
+          v.z = __byte_perm(pr[0], pr[1], 0x7632);
+          v.w = __byte_perm(pr[2], pr[3], 0x7632);
+          const int blk = (u4 & 1) * 4 + j;
+          *reinterpret_cast<uint4*>(tilep + r * 128 + ((blk ^ (r & 7)) << 4)) = v;
+        }
+      }
+      tc::fence_proxy_async_smem();
+      tc::mbar_arrive(&a_full[sa]);
+      if (c + 1 < c1 - c0) load(c + 1);
+    }
+  } else {
+    if constexpr (kN > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    // scale and add: thread = row, this warp's half of the tokens
+    const int half = (warp - 8) >> 2;
+    const int64_t row = row0 + (warp & 3) * 32 + lane;
+    const int64_t r = min(row, a.l.m - 1);
+    const int G = gs ? (int)((a.l.n + gs - 1) / gs) : 1;
+    const float* sp = a.l.scales + r * G;
+    const int gfirst = gs ? c0 * kChunk / gs : 0;
+    uint64_t acc[kN / 4];
+#pragma unroll
+    for (int j = 0; j < kN / 4; ++j) acc[j] = 0;
+    bool ok = true;
+    float s_next = __ldg(sp + min(gfirst, G - 1));
+    const uint32_t tcol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * (N / 2);
+    for (int p = 0; p < periods; ++p) {
+      const float s = s_next;
+      if (gs && p + 1 < periods) s_next = __ldg(sp + min(gfirst + p + 1, G - 1));
+      if (!wait_or_fail(&t_full[p & 1], (p >> 1) & 1, fail)) { ok = false; break; }
+      tc::fence_after_sync();
+      uint64_t s2;
+      asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+#pragma unroll
+      for (int cb = 0; cb < kN / 64; ++cb) {
+        if (cb * 32 < N / 2) {
+          float v[32];
+          tc::tmem_ld32(tcol + (p & 1) * kN + cb * 32, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) fma2(acc[cb * 16 + e], v[2 * e], v[2 * e + 1], s2);
+        }
+      }
+      tc::fence_before_sync();
+      tc::mbar_arrive(&t_empty[p & 1]);
+    }
+    auto store = [&](int64_t tok, int64_t rr, float v) {
+      if (tok < a.l.T && rr < a.l.m) {
+        if (a.l.xscale) v *= __ldg(a.l.xscale + tok);
+        if (a.l.y_bf16)
+          static_cast<__nv_bfloat16*>(a.l.y)[tok * a.l.m + rr] = __float2bfloat16(v);
+        else
+          static_cast<float*>(a.l.y)[tok * a.l.m + rr] = v;
+      }
+    };
+    if (!ok) {
+      if (lane == 0) record_status(a.hdr, GQ_ERR_TIMEOUT);
+    } else if (S == 1) {
+#pragma unroll
+      for (int e = 0; e < kN / 4; ++e) {
+        if (2 * e < N / 2) {
+          const float2 v = *reinterpret_cast<const float2*>(&acc[e]);
+          store(t0 + half * (N / 2) + 2 * e, row, v.x);
+          store(t0 + half * (N / 2) + 2 * e + 1, row, v.y);
+        }
+      }
+    } else {
+      // partial sums as [token][row] over the operand rings (every MMA of this CTA is complete:
+      // its last accumulator has been read)
+      float* part = reinterpret_cast<float*>(base);
+#pragma unroll
+      for (int e = 0; e < kN / 4; ++e) {
+        if (2 * e < N / 2) {
+          const float2 v = *reinterpret_cast<const float2*>(&acc[e]);
+          float* q = part + (half * (N / 2) + 2 * e) * 128 + (warp & 3) * 32 + lane;
+          q[0] = v.x;
+          q[128] = v.y;
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  // Back to the launch's register share for the common end.  Only behind the barrier: the two
+  // smaller shares may not grow before the larger one has been taken and given back, or it could
+  // never be taken.
+  if constexpr (kN > 128) {
+    if (warp >= 8)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+  }
+  if (warp == 1 && lane == 0) tc::mbar_wait(done, 0);  // also after a failure: no MMA in flight
+  __syncwarp();
+  if (S > 1) {
+    cluster_sync();
+    // this CTA adds the parts of its share of the tokens, in the order of the ranks
+    const uint32_t part = tc::smem_u32(base);
+    const int n0 = (int)((int64_t)N * rank / S), n1 = (int)((int64_t)N * (rank + 1) / S);
+    for (int i = n0 * 128 + tid; i < n1 * 128; i += kLinThreads) {
+      float v = 0.f;
+      for (uint32_t q = 0; q < S; ++q) v += ld_cluster_f32(part + i * 4, q);
+      const int64_t tok = t0 + i / 128, rr = row0 + i % 128;
+      if (tok < a.l.T && rr < a.l.m) {
+        if (a.l.xscale) v *= __ldg(a.l.xscale + tok);
+        if (a.l.y_bf16)
+          static_cast<__nv_bfloat16*>(a.l.y)[tok * a.l.m + rr] = __float2bfloat16(v);
+        else
+          static_cast<float*>(a.l.y)[tok * a.l.m + rr] = v;
+      }
+    }
+    cluster_sync();  // the parts stay until every CTA of the cluster has read them
+  }
+  __syncthreads();
+  if (warp == 2) tc::tmem_dealloc(tmem, 2 * kN);
+}
+
+// ---- tokens as bf16 parts: P x T rows of ld elements, columns behind n zero ----
+template <LinearInput K>
+__global__ void linear_stage_kernel(const void* __restrict__ x, int64_t T, int64_t n, int64_t ld,
+                                    const int32_t* __restrict__ perm, uint16_t* __restrict__ out) {
+  const int64_t t = blockIdx.x;
+  for (int64_t k = threadIdx.x; k < ld; k += blockDim.x) {
+    const int64_t src = t * n + (k < n ? (perm ? perm_at(perm, k, n) : k) : 0);
+    uint16_t* o = out + t * ld + k;
+    if constexpr (K == kXFp32) {
+      const float v = k < n ? static_cast<const float*>(x)[src] : 0.f;
+      uint32_t h, m, l;
+      split3(v, h, m, l);
+      o[0] = (uint16_t)(h >> 16);
+      o[T * ld] = (uint16_t)(m >> 16);
+      o[2 * T * ld] = (uint16_t)(l >> 16);
+    } else if constexpr (K == kXInt8) {
+      const float v = k < n ? (float)static_cast<const int8_t*>(x)[src] : 0.f;
+      o[0] = __bfloat16_as_ushort(__float2bfloat16(v));
+    } else {
+      o[0] = k < n ? static_cast<const uint16_t*>(x)[src] : (uint16_t)0;
+    }
+  }
+}
+
+namespace {
+// What a call does: whether the tokens are staged, the tile and the split of the columns.
+struct LinPlan {
+  bool tc, staged;
+  int P;
+  int64_t ld;      // staged row length, elements
+};
+LinPlan plan_of(int64_t T, int64_t n, LinearInput kind, bool ordered) {
+  LinPlan p{};
+  p.tc = T > 32;
+  p.P = kind == kXFp32 ? 3 : 1;
+  // TMA takes rows whose length is a multiple of 16 bytes
+  p.staged = kind != kXBf16 || ordered || n % 8 != 0;
+  p.ld = (n + 63) / 64 * 64;
+  return p;
+}
+
+template <int B, int P, int kN>
+cudaError_t launch_tc(const CUtensorMap& map, const LinTcArgs& a, int vec, int S, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.mtiles * a.ntiles * S));
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = kLinSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)S;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<B, P, kN>, map, a, vec);
+}
+template <int B>
+cudaError_t launch_tc_bits(const CUtensorMap& map, const LinTcArgs& a, int P, int kN, int vec,
+                           int S, cudaStream_t s) {
+  if (P == 3) return launch_tc<B, 3, 128>(map, a, vec, S, s);
+  return kN == 128 ? launch_tc<B, 1, 128>(map, a, vec, S, s)
+                   : launch_tc<B, 1, 256>(map, a, vec, S, s);
+}
+template <int B>
+cudaError_t init_bits() {
+  cudaError_t e;
+  cudaFuncAttributes at;
+  if ((e = cudaFuncSetAttribute(linear_tc_kernel<B, 3, 128>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem)))
+    return e;
+  if ((e = cudaFuncSetAttribute(linear_tc_kernel<B, 1, 128>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem)))
+    return e;
+  if ((e = cudaFuncSetAttribute(linear_tc_kernel<B, 1, 256>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem)))
+    return e;
+  if ((e = cudaFuncGetAttributes(&at, linear_tc_kernel<B, 1, 256>))) return e;
+  // the warpgroups' register shares (40 + 112 + 2 x 176) have to fit the launch's registers
+  return at.numRegs >= 126 ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+}  // namespace
+
+size_t linear_ws_bytes(int64_t T, int64_t n, LinearInput kind, bool ordered) {
+  const LinPlan p = plan_of(T, n, kind, ordered);
+  if (!p.tc) return 0;
+  return kAlign + (p.staged ? align_up((size_t)p.P * T * p.ld * 2) : 0);
+}
+
+cudaError_t linear_init_attributes() {
+  cudaError_t e;
+  if ((e = init_bits<2>())) return e;
+  if ((e = init_bits<3>())) return e;
+  if ((e = init_bits<4>())) return e;
+  if ((e = init_bits<5>())) return e;
+  if ((e = init_bits<6>())) return e;
+  if ((e = init_bits<7>())) return e;
+  return init_bits<8>();
+}
+
+cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  const LinPlan p = plan_of(a.T, a.n, kind, a.perm != nullptr);
+  // a misaligned matrix cannot be a tensor map: the warp-level kernel reads it in place
+  const bool aligned = p.staged || reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
+  const int64_t rows_total = (int64_t)p.P * a.T;
+  if (!p.tc || !aligned || rows_total > INT32_MAX) return launch_linear_rows(a, kind, s);
+  const void* xt = a.x;
+  int64_t ld = a.n, cols = a.n;
+  if (p.staged) {
+    uint16_t* out = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kAlign);
+    const unsigned grid = (unsigned)a.T;
+    if (kind == kXFp32)
+      linear_stage_kernel<kXFp32><<<grid, 256, 0, s>>>(a.x, a.T, a.n, p.ld, a.perm, out);
+    else if (kind == kXInt8)
+      linear_stage_kernel<kXInt8><<<grid, 256, 0, s>>>(a.x, a.T, a.n, p.ld, a.perm, out);
+    else
+      linear_stage_kernel<kXBf16><<<grid, 256, 0, s>>>(a.x, a.T, a.n, p.ld, a.perm, out);
+    count_launches(1);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    xt = out;
+    ld = cols = p.ld;
+  }
+  LinTcArgs t{};
+  t.l = a;
+  t.l.perm = nullptr;
+  t.planes_t = p.P > 1 ? (int)a.T : 0;
+  const int kN = p.P == 1 && a.T > 128 ? 256 : 128;
+  t.N = (int)(a.T >= kN ? kN : (a.T + 63) / 64 * 64);
+  t.mtiles = (int)((a.m + 127) / 128);
+  t.ntiles = (int)((a.T + t.N - 1) / t.N);
+  t.chunks = (int)((a.n + kChunk - 1) / kChunk);
+  t.hdr = static_cast<WsHeader*>(ws);
+  const int64_t tiles = (int64_t)t.mtiles * t.ntiles;
+  if (tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
+  // columns shared by a cluster while tiles leave SMs idle and every CTA keeps four chunks
+  int S = 1;
+  while (S < 8 && tiles * S * 2 <= 148 && t.chunks >= S * 8) S *= 2;
+  CUtensorMap map;
+  cudaError_t e = encode_tmap_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, xt, rows_total, cols,
+                                 ld, 64, (uint32_t)t.N, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  // widest loads of the packed words: rows start on 16-byte (8-byte) boundaries
+  const int64_t words = row_words(a.n, a.bits);
+  const int vec = words % 4 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 16 == 0;
+  switch (a.bits) {
+    case 2: e = launch_tc_bits<2>(map, t, p.P, kN, vec, S, s); break;
+    case 3: e = launch_tc_bits<3>(map, t, p.P, kN, vec, S, s); break;
+    case 4: e = launch_tc_bits<4>(map, t, p.P, kN, vec, S, s); break;
+    case 5: e = launch_tc_bits<5>(map, t, p.P, kN, vec, S, s); break;
+    case 6: e = launch_tc_bits<6>(map, t, p.P, kN, vec, S, s); break;
+    case 7: e = launch_tc_bits<7>(map, t, p.P, kN, vec, S, s); break;
+    default: e = launch_tc_bits<8>(map, t, p.P, kN, vec, S, s); break;
+  }
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace gq

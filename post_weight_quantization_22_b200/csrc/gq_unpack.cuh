@@ -80,6 +80,14 @@ __device__ __forceinline__ uint32_t pair_value(uint32_t p, uint32_t zp) {
   }
 }
 
+// Three bf16 parts of an fp32 value, by truncation: their sum is the value (8 + 8 + 8 bits).
+__device__ __forceinline__ void split3(float v, uint32_t& h, uint32_t& mid, uint32_t& low) {
+  h = __float_as_uint(v) & 0xFFFF0000u;
+  const float r = fabsf(v) == __int_as_float(0x7F800000) ? 0.f : v - __uint_as_float(h);
+  mid = __float_as_uint(r) & 0xFFFF0000u;
+  low = __float_as_uint(r - __uint_as_float(mid));
+}
+
 // Words of a row's stream.
 __host__ __device__ __forceinline__ int64_t row_words(int64_t n, int bits) {
   return (n * bits + 31) / 32;

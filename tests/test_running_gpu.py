@@ -392,3 +392,19 @@ def test_norm_feeds_the_product():
         # and the rows are within half a step of the norm
         got = r["q"].double().cpu().numpy() * r["qscale"].double().cpu().numpy()[:, None]
         assert np.all(np.abs(got - v) <= (0.5 + 127 * 2.0 ** -23) * qs[:, None])
+
+
+@pytest.mark.parametrize("dtype", (torch.bfloat16, torch.int8))
+def test_more_tiles_than_sms(dtype):
+    """Several tiles one after another on every SM."""
+    from post_weight_quantization_22_b200 import gq as G
+    m, n, bits, group, T = 2500, 200, 4, 32, 5000
+    c, s, z, w = layer_np(m, n, bits, group, 12)
+    dev = to_cuda(c, s, z, bits)
+    if dtype == torch.int8:
+        q, qs = _rows(T, n, 1)
+        y = G.gq_linear_quantized(q, qs, *dev, bits, group)
+        check_linear(y, q.double().cpu().numpy(), w, qs.double().cpu().numpy())
+    else:
+        x = _x(T, n, dtype, 1)
+        check_linear(G.gq_linear(x, *dev, bits, group), x.double().cpu().numpy(), w)
