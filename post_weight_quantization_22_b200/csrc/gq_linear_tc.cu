@@ -9,9 +9,11 @@
 // group is multiplied.  No weight is rounded, and no chain of tensor-core additions is longer
 // than 256 columns.
 //
-// Roles: warp 0 the tokens' TMA loads, warp 1 the MMAs, warps 4-7 unpack, warps 8-15 scale and
-// add.  With fewer tiles than SMs a cluster shares one tile's columns, and its CTAs add their
-// sums over distributed shared memory in a fixed order.
+// Roles: warp 0 the tokens' TMA loads, warp 1 the MMAs, warps 4-11 unpack, warps 12-19 scale and
+// add.  CTAs are persistent: they take tile after tile, and the next tile's columns are unpacked
+// and multiplied while the last one's sums are stored.  With fewer tiles than SMs a cluster
+// shares one tile's columns, and its CTAs add their sums over distributed shared memory in a
+// fixed order.
 #include "gq_internal.cuh"
 #include "gq_tc.cuh"
 #include "gq_unpack.cuh"
@@ -19,20 +21,33 @@
 namespace gq {
 
 namespace {
-constexpr int kLinThreads = 512;
+constexpr int kLinThreads = 640;
+constexpr int kUnpackWarp = 4, kScaleWarp = 12;   // first warps of these roles, 8 each
+// Registers a thread of the three roles holds, in warpgroups of 128 threads: together what the
+// launch has (96 x 640).  A scaling thread holds 128 sums.
+#define GQ_LIN_REGS_CONTROL "32"
+#define GQ_LIN_REGS_UNPACK "56"
+#define GQ_LIN_REGS_SCALE "168"
+#define GQ_LIN_REGS_LAUNCH "96"
+constexpr int kSMs = 148;
 constexpr int kChunk = 128;                       // columns per A slot
 constexpr uint32_t kASub = 128 * 64 * 2;          // 64 columns of 128 rows
 constexpr uint32_t kASlot = 2 * kASub;
 constexpr int kASlots = 2;
 constexpr uint32_t kBRing = 128 * 1024;
-constexpr size_t kLinSmem = kASlots * kASlot + kBRing + 1024 + 512;
+constexpr uint32_t kOutStage = 2048;              // a scaling warp's output staging
+constexpr size_t kLinSmem = kASlots * kASlot + kBRing + 8 * kOutStage + 1024 + 512;
 
 struct LinTcArgs {
   LinearArgs l;
   int planes_t;      // rows between two parts of the tokens (0 with one part)
   int N;             // tokens per tile
   int mtiles, ntiles;
+  int tiles;         // mtiles * ntiles
   int chunks;        // chunks of 128 columns
+  int gshift;        // log2 of the group width (31: one grid per row, every index is 0)
+  int dmask;         // 16-column steps per accumulator period (a power of two) - 1
+  int groups;        // groups of a row
   WsHeader* hdr;
 };
 
@@ -46,10 +61,69 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, vol
   return false;
 }
 
+// The same for a whole warp: one lane polls.  (32 polls, or 32 arrivals, on one barrier are
+// serialised in shared memory: at 384 of them a chunk they cost more than the chunk's MMAs.)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_or_fail(bar, parity, fail);
+  return __shfl_sync(~0u, ok, 0) != 0;
+}
+// One arrival for a whole warp (its barriers count warps).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
 __device__ __forceinline__ void fma2(uint64_t& acc, float a, float b, uint64_t s) {
   uint64_t v;
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
+}
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16(v); }
+// A warp's 32 rows x 2 E tokens of sums into y (T x m; y at the warp's first row and token): rows
+// < rows and tokens < cnt are written, times the tokens' scales xs (null: 1).  With rows of y on
+// 16-byte boundaries the values go through shared memory, so that a lane stores 16 bytes (one
+// 2-byte store per value took 11 cycles a warp instruction, a third of a 4096-column tile's time).
+template <int E, class Y>
+__device__ __forceinline__ void store_tile(Y* y, int64_t ld, const uint64_t (&acc)[E], int cnt,
+                                           int rows, const float* __restrict__ xs, bool wide,
+                                           uint8_t* stage, int lane) {
+  constexpr int kTok = (int)(kOutStage / (32 * sizeof(Y)));  // tokens per staging pass
+  constexpr int kVec = 16 / (int)sizeof(Y);                  // values in 16 bytes
+  constexpr int kPer = 32 / kVec;                            // lanes per token
+  Y* st = reinterpret_cast<Y*>(stage);
+#pragma unroll
+  for (int b = 0; b < 2 * E / kTok; ++b) {
+    if (b * kTok >= cnt) break;
+    if (wide) {
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) {
+        const float2 v2 = *reinterpret_cast<const float2*>(&acc[(b * kTok + j) / 2]);
+        float v = (j & 1) ? v2.y : v2.x;
+        if (xs && b * kTok + j < cnt) v *= __ldg(xs + b * kTok + j);
+        put(st + j * 32 + lane, v);
+      }
+      __syncwarp();
+      const int r = (lane % kPer) * kVec;
+#pragma unroll
+      for (int i = 0; i < kTok * kPer / 32; ++i) {
+        const int j = i * (32 / kPer) + lane / kPer;
+        const uint4 v = *reinterpret_cast<const uint4*>(st + j * 32 + r);
+        if (b * kTok + j < cnt && r < rows)
+          *reinterpret_cast<uint4*>(y + (b * kTok + j) * ld + r) = v;
+      }
+      __syncwarp();
+    } else if (lane < rows) {
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) {
+        const float2 v2 = *reinterpret_cast<const float2*>(&acc[(b * kTok + j) / 2]);
+        const float v = (j & 1) ? v2.y : v2.x;
+        if (b * kTok + j < cnt)
+          put(y + (b * kTok + j) * ld + lane, xs ? v * __ldg(xs + b * kTok + j) : v);
+      }
+    }
+  }
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -101,10 +175,11 @@ __device__ __forceinline__ void load_unit(const uint32_t* __restrict__ row, int 
 }
 }  // namespace
 
-// kN: the largest N; P: parts of the tokens (3 for fp32).
+// kN: the largest N; P: parts of the tokens (3 for fp32).  vec: the packed rows allow wide loads;
+// wide: rows of y are on 16-byte boundaries.
 template <int B, int P, int kN>
 __global__ void __launch_bounds__(kLinThreads, 1)
-    linear_tc_kernel(const __grid_constant__ CUtensorMap m_x, LinTcArgs a, int vec) {
+    linear_tc_kernel(const __grid_constant__ CUtensorMap m_x, LinTcArgs a, int vec, int wide) {
   constexpr uint32_t kBSlot = kN * 128;
   constexpr int kBSlots = (int)(kBRing / kBSlot);
   static_assert(kBSlots >= P + 1, "the parts of one step have to fit the ring");
@@ -112,7 +187,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(lin_smem) + 1023) & ~uintptr_t(1023));
   uint8_t* bring = base + kASlots * kASlot;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(bring + kBRing);
+  uint8_t* ostage = bring + kBRing;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ostage + 8 * kOutStage);
   uint64_t* a_full = bars;
   uint64_t* a_empty = a_full + kASlots;
   uint64_t* b_full = a_empty + kASlots;
@@ -125,25 +201,20 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t S = cluster_size(), rank = cluster_rank();
-  const unsigned tile = blockIdx.x / S;
-  const int mt = (int)(tile % (unsigned)a.mtiles);
-  const int64_t row0 = (int64_t)mt * 128;
-  const int64_t t0 = (int64_t)(tile / (unsigned)a.mtiles) * a.N;
+  const int tile0 = (int)(blockIdx.x / S), tstep = (int)(gridDim.x / S);
   const int N = a.N;
   // this CTA's chunks; pairs of chunks stay together (a period may span two)
   const int pairs = (a.chunks + 1) / 2;
   const int c0 = 2 * (int)((int64_t)pairs * rank / S);
-  const int c1 = min(a.chunks, 2 * (int)((int64_t)pairs * (rank + 1) / S));
-  const int gs = a.l.group;
-  const int dk = gs ? gs / 16 : 16;               // 16-column steps per accumulator period
-  const int steps = (c1 - c0) * 8;
-  const int periods = (steps + dk - 1) / dk;
+  const int nc = min(a.chunks, 2 * (int)((int64_t)pairs * (rank + 1) / S)) - c0;
+  const int steps = nc * 8;                                        // of 16 columns, a tile
+  const int periods = (steps + a.dmask) / (a.dmask + 1);           // a tile
 
   if (blockIdx.x == 0 && tid == 0) a.hdr->status = 0;  // no wait can run out for a second yet
   if (tid == 0) {
-    for (int i = 0; i < kASlots; ++i) { tc::mbar_init(&a_full[i], 128); tc::mbar_init(&a_empty[i], 1); }
+    for (int i = 0; i < kASlots; ++i) { tc::mbar_init(&a_full[i], 8); tc::mbar_init(&a_empty[i], 1); }
     for (int i = 0; i < kBSlots; ++i) { tc::mbar_init(&b_full[i], 1); tc::mbar_init(&b_empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { tc::mbar_init(&t_full[i], 1); tc::mbar_init(&t_empty[i], 256); }
+    for (int i = 0; i < 2; ++i) { tc::mbar_init(&t_full[i], 1); tc::mbar_init(&t_empty[i], 8); }
     tc::mbar_init(done, 1);
     *fail = 0;
     tc::fence_barrier_init();
@@ -155,197 +226,243 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *tslot;
 
-  if (warp < 4) {
-    if constexpr (kN > 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 0 && lane == 0) {
-      // tokens: 64 columns of every part per step of the ring
-      int i = 0;
-      const int subs = (c1 - c0) * 2;
-      bool ok = true;
-      for (int sub = 0; sub < subs && ok; ++sub) {
+  if (warp < kUnpackWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 " GQ_LIN_REGS_CONTROL ";");
+    if (warp == 0) {
+      if (tc::elect_one()) {
+        // tokens: 64 columns of every part per step of the ring
+        int i = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < a.tiles && ok; tile += tstep) {
+          const int64_t t0 = (int64_t)(tile / a.mtiles) * N;
+          for (int sub = 0; sub < 2 * nc && ok; ++sub) {
 #pragma unroll
-        for (int p = 0; p < P; ++p, ++i) {
-          const int s = i % kBSlots;
-          if (i >= kBSlots && !wait_or_fail(&b_empty[s], ((i / kBSlots) - 1) & 1, fail)) {
-            ok = false;
-            break;
-          }
-          tc::mbar_arrive_expect_tx(&b_full[s], (uint32_t)N * 128);
-          tc::tma_load_2d(bring + s * kBSlot, &m_x, &b_full[s], c0 * kChunk + sub * 64,
-                          (int)(t0 + (int64_t)p * a.planes_t));
-        }
-      }
-      if (!ok)  // no copy may be in flight when the CTA ends
-        for (int j = max(0, i - kBSlots); j < i; ++j)
-          tc::mbar_wait(&b_full[j % kBSlots], (j / kBSlots) & 1);
-    } else if (warp == 1 && lane == 0) {
-      const uint32_t idesc = tc::idesc_f32acc(1, 1, 0, 0, 128, (uint32_t)N);
-      int i = 0, step = 0, period = 0;
-      bool ok = true;
-      for (int c = 0; c < c1 - c0 && ok; ++c) {
-        const int sa = c % kASlots;
-        if (!wait_or_fail(&a_full[sa], (c / kASlots) & 1, fail)) break;
-        for (int sub = 0; sub < 2 && ok; ++sub) {
-          for (int p = 0; p < P; ++p)
-            ok = ok && wait_or_fail(&b_full[(i + p) % kBSlots], ((i + p) / kBSlots) & 1, fail);
-          if (!ok) break;
-          tc::fence_after_sync();
-          const uint32_t at = tc::smem_u32(base + sa * kASlot + sub * kASub);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int buf = period & 1;
-            const bool first = step % dk == 0;
-            if (first && period >= 2) {
-              ok = ok && wait_or_fail(&t_empty[buf], ((period >> 1) - 1) & 1, fail);
-              tc::fence_after_sync();
-            }
-            if (ok) {
-              const uint64_t da = tc::sdesc(at + k * 32, 16, 1024, tc::kLayoutSW128);
-              for (int p = 0; p < P; ++p) {
-                const uint32_t bt = tc::smem_u32(bring + ((i + p) % kBSlots) * kBSlot);
-                const uint64_t db = tc::sdesc(bt + k * 32, 16, 1024, tc::kLayoutSW128);
-                tc::mma_f16(tmem + buf * kN, da, db, idesc, !(first && p == 0));
+            for (int p = 0; p < P; ++p, ++i) {
+              const int s = i % kBSlots;
+              if (i >= kBSlots && !wait_or_fail(&b_empty[s], ((i / kBSlots) - 1) & 1, fail)) {
+                ok = false;
+                break;
               }
-            }
-            ++step;
-            if (ok && (step % dk == 0 || step == steps)) {
-              tc::mma_commit(&t_full[buf]);
-              ++period;
+              tc::mbar_arrive_expect_tx(&b_full[s], (uint32_t)N * 128);
+              tc::tma_load_2d(bring + s * kBSlot, &m_x, &b_full[s], c0 * kChunk + sub * 64,
+                              (int)(t0 + (int64_t)p * a.planes_t));
             }
           }
-          for (int p = 0; p < P; ++p, ++i) tc::mma_commit(&b_empty[i % kBSlots]);
         }
-        tc::mma_commit(&a_empty[sa]);
+        if (!ok)  // no copy may be in flight when the CTA ends
+          for (int j = max(0, i - kBSlots); j < i; ++j)
+            tc::mbar_wait(&b_full[j % kBSlots], (j / kBSlots) & 1);
       }
-      tc::mma_commit(done);
+    } else if (warp == 1) {
+      if (tc::elect_one()) {
+        // One thread issues every MMA; a step of 16 columns takes the tensor cores 128 cycles, so
+        // what surrounds it has to be short: descriptors differ in their address field alone,
+        // and the counters are masks.
+        const uint32_t idesc = tc::idesc_f32acc(1, 1, 0, 0, 128, (uint32_t)N);
+        const uint64_t dbase = tc::sdesc(0, 16, 1024, tc::kLayoutSW128);
+        const uint32_t a_at = tc::smem_u32(base) >> 4, b_at = tc::smem_u32(bring) >> 4;
+        const int dmask = a.dmask;
+        int i = 0, ca = 0, period = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < a.tiles && ok; tile += tstep) {
+          int step = 0;
+          for (int c = 0; c < nc && ok; ++c, ++ca) {
+            const int sa = ca % kASlots;
+            ok = wait_or_fail(&a_full[sa], (ca / kASlots) & 1, fail);
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+              uint64_t db[P];
+#pragma unroll
+              for (int p = 0; p < P; ++p) {
+                const int s = (i + p) % kBSlots;
+                ok = ok && wait_or_fail(&b_full[s], ((i + p) / kBSlots) & 1, fail);
+                db[p] = dbase + (b_at + s * (kBSlot >> 4));
+              }
+              const uint64_t da = dbase + (a_at + sa * (kASlot >> 4) + sub * (kASub >> 4));
+              if (dmask >= 3) {  // a period is one or more of these 64 columns
+                const bool first = (step & dmask) == 0;
+                if (first && period >= 2)
+                  ok = ok && wait_or_fail(&t_empty[period & 1], ((period >> 1) - 1) & 1, fail);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t d = tmem + (period & 1) * kN;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                  for (int p = 0; p < P; ++p)
+                    tc::mma_f16(d, da + 2 * k, db[p] + 2 * k, idesc, k > 0 || p > 0 || !first);
+                step += 4;
+                if ((step & dmask) == 0 || step == steps) {
+                  tc::mma_commit(&t_full[period & 1]);
+                  ++period;
+                }
+              } else {  // groups of 16 or 32 columns: several periods in them
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const bool first = (step & dmask) == 0;
+                  if (first && period >= 2)
+                    ok = ok && wait_or_fail(&t_empty[period & 1], ((period >> 1) - 1) & 1, fail);
+                  if (!ok) break;
+                  tc::fence_after_sync();
+                  const uint32_t d = tmem + (period & 1) * kN;
+#pragma unroll
+                  for (int p = 0; p < P; ++p)
+                    tc::mma_f16(d, da + 2 * k, db[p] + 2 * k, idesc, p > 0 || !first);
+                  ++step;
+                  if ((step & dmask) == 0) {
+                    tc::mma_commit(&t_full[period & 1]);
+                    ++period;
+                  }
+                }
+                if (!ok) break;
+              }
+#pragma unroll
+              for (int p = 0; p < P; ++p, ++i) tc::mma_commit(&b_empty[i % kBSlots]);
+            }
+            if (ok) tc::mma_commit(&a_empty[sa]);
+          }
+        }
+        tc::mma_commit(done);
+      }
     }
     __syncwarp();
-  } else if (warp < 8) {
-    if constexpr (kN > 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-    // unpack: a thread takes one unit of 32 columns of rows 8 i + lane % 8, i = 0..3, of its
-    // warp's 32 rows (a warp reads 8 rows x 16 b bytes at a time; its 16-byte stores of one
+  } else if (warp < kScaleWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 " GQ_LIN_REGS_UNPACK ";");
+    // unpack: a thread takes one unit of 32 columns of rows 8 i + lane % 8, i = 0, 1, of its
+    // warp's 16 rows (a warp reads 8 rows x 16 b bytes at a time; its 16-byte stores of one
     // column block fall on 8 different rows, so the swizzled tile takes them without conflicts)
     const int words = (int)row_words(a.l.n, B);
-    const int G = gs ? (int)((a.l.n + gs - 1) / gs) : 1;
+    const int G = a.groups, gsh = a.gshift;
     const int u4 = lane >> 3;
-    const uint32_t* rp[4];
-    const uint8_t* zp[4];
-    uint32_t w[4][B], z[4][2];
-    const int r_in = (warp - 4) * 32 + (lane & 7);
+    const int r_in = (warp - kUnpackWarp) * 16 + (lane & 7);
+    const uint32_t* rp[2];
+    const uint8_t* zp[2];
+    uint32_t w[2][B], z[2][2];
+    auto rows_of = [&](int tile) {
+      const int64_t row0 = (int64_t)(tile % a.mtiles) * 128;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = min(row0 + r_in + 8 * i, a.l.m - 1);
-      rp[i] = a.l.codes + r * words;
-      zp[i] = a.l.zeros + r * G;
-    }
-    auto load = [&](int c) {
-      const int unit = (c0 + c) * 4 + u4;
-      const int g0 = gs ? min(unit * 32 / gs, G - 1) : 0;
-      const int g1 = gs == 16 ? min(unit * 2 + 1, G - 1) : g0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        load_unit<B>(rp[i], unit, words, vec, w[i]);
-        z[i][0] = __ldg(zp[i] + g0);
-        z[i][1] = gs == 16 ? __ldg(zp[i] + g1) : z[i][0];
+      for (int i = 0; i < 2; ++i) {
+        const int64_t r = min(row0 + r_in + 8 * i, a.l.m - 1);
+        rp[i] = a.l.codes + r * words;
+        zp[i] = a.l.zeros + r * G;
       }
     };
-    if (c1 > c0) load(0);
-    for (int c = 0; c < c1 - c0; ++c) {
-      const int sa = c % kASlots;
-      if (c >= kASlots && !wait_or_fail(&a_empty[sa], ((c / kASlots) - 1) & 1, fail)) break;
-      uint8_t* tilep = base + sa * kASlot + (u4 >> 1) * kASub;
+    auto load = [&](int c, int i) {
+      const int unit = (c0 + c) * 4 + u4;
+      const int g0 = min((unit * 32) >> gsh, G - 1);
+      load_unit<B>(rp[i], unit, words, vec, w[i]);
+      z[i][0] = __ldg(zp[i] + g0);
+      z[i][1] = gsh == 4 ? __ldg(zp[i] + min(g0 + 1, G - 1)) : z[i][0];
+    };
+    rows_of(tile0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r_in + 8 * i;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // eight columns
-          constexpr int kTop = B - 1;
-          const int q = (j * B) / 4, sh = 8 * ((j * B) % 4);
-          const uint32_t w0 = w[i][q], w1 = w[i][q + 1 < B ? q + 1 : kTop];
-          const uint32_t w2 = w[i][q + 2 < B ? q + 2 : kTop];
-          uint32_t pr[4];
-          code_pairs<B>(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh), pr);
-          const uint32_t zz = zero_pair<B, false>(z[i][j >> 1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pr[e] = pair_value<B, false>(pr[e], zz);
-          uint4 v;  // from pairs (e, e + 4) to columns in order
-          v.x = __byte_perm(pr[0], pr[1], 0x5410);
-          v.y = __byte_perm(pr[2], pr[3], 0x5410);
-          v.z = __byte_perm(pr[0], pr[1], 0x7632);
-          v.w = __byte_perm(pr[2], pr[3], 0x7632);
-          const int blk = (u4 & 1) * 4 + j;
-          *reinterpret_cast<uint4*>(tilep + r * 128 + ((blk ^ (r & 7)) << 4)) = v;
+    for (int i = 0; i < 2; ++i) load(0, i);
+    int ca = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < a.tiles && ok; tile += tstep) {
+      for (int c = 0; c < nc; ++c, ++ca) {
+        const int sa = ca % kASlots;
+        if (ca >= kASlots && !warp_wait(&a_empty[sa], ((ca / kASlots) - 1) & 1, fail)) {
+          ok = false;
+          break;
         }
+        uint8_t* tilep = base + sa * kASlot + (u4 >> 1) * kASub;
+        const bool next_tile = c + 1 == nc;
+        const bool more = !next_tile || tile + tstep < a.tiles;
+        if (next_tile && more) rows_of(tile + tstep);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = r_in + 8 * i;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // eight columns
+            constexpr int kTop = B - 1;
+            const int q = (j * B) / 4, sh = 8 * ((j * B) % 4);
+            const uint32_t w0 = w[i][q], w1 = w[i][q + 1 < B ? q + 1 : kTop];
+            const uint32_t w2 = w[i][q + 2 < B ? q + 2 : kTop];
+            uint32_t pr[4];
+            code_pairs<B>(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh), pr);
+            const uint32_t zz = zero_pair<B, false>(z[i][j >> 1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pr[e] = pair_value<B, false>(pr[e], zz);
+            uint4 v;  // from pairs (e, e + 4) to columns in order
+            v.x = __byte_perm(pr[0], pr[1], 0x5410);
+            v.y = __byte_perm(pr[2], pr[3], 0x5410);
+            v.z = __byte_perm(pr[0], pr[1], 0x7632);
+            v.w = __byte_perm(pr[2], pr[3], 0x7632);
+            const int blk = (u4 & 1) * 4 + j;
+            *reinterpret_cast<uint4*>(tilep + r * 128 + ((blk ^ (r & 7)) << 4)) = v;
+          }
+          if (more) load(next_tile ? 0 : c + 1, i);  // in flight for a whole chunk
+        }
+        tc::fence_proxy_async_smem();
+        warp_arrive(&a_full[sa]);
       }
-      tc::fence_proxy_async_smem();
-      tc::mbar_arrive(&a_full[sa]);
-      if (c + 1 < c1 - c0) load(c + 1);
     }
   } else {
-    if constexpr (kN > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 " GQ_LIN_REGS_SCALE ";");
     // scale and add: thread = row, this warp's half of the tokens
-    const int half = (warp - 8) >> 2;
-    const int64_t row = row0 + (warp & 3) * 32 + lane;
-    const int64_t r = min(row, a.l.m - 1);
-    const int G = gs ? (int)((a.l.n + gs - 1) / gs) : 1;
-    const float* sp = a.l.scales + r * G;
-    const int gfirst = gs ? c0 * kChunk / gs : 0;
-    uint64_t acc[kN / 4];
-#pragma unroll
-    for (int j = 0; j < kN / 4; ++j) acc[j] = 0;
+    const int half = (warp - kScaleWarp) >> 2, quarter = warp & 3;
+    const int G = a.groups;
+    const bool grid1 = a.gshift == 31;  // one scale per row
+    const int gfirst = (c0 * kChunk) >> a.gshift;
+    const uint32_t tcol = tmem + ((uint32_t)(quarter * 32) << 16) + half * (N / 2);
+    int pt = 0;  // periods of all tiles
     bool ok = true;
-    float s_next = __ldg(sp + min(gfirst, G - 1));
-    const uint32_t tcol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * (N / 2);
-    for (int p = 0; p < periods; ++p) {
-      const float s = s_next;
-      if (gs && p + 1 < periods) s_next = __ldg(sp + min(gfirst + p + 1, G - 1));
-      if (!wait_or_fail(&t_full[p & 1], (p >> 1) & 1, fail)) { ok = false; break; }
-      tc::fence_after_sync();
-      uint64_t s2;
-      asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+    for (int tile = tile0; tile < a.tiles && ok; tile += tstep) {
+      const int64_t row0 = (int64_t)(tile % a.mtiles) * 128 + quarter * 32;  // this warp's
+      const int64_t tk = (int64_t)(tile / a.mtiles) * N + half * (N / 2);
+      const float* sp = a.l.scales + min(row0 + lane, a.l.m - 1) * G;
+      uint64_t acc[kN / 4];
 #pragma unroll
-      for (int cb = 0; cb < kN / 64; ++cb) {
-        if (cb * 32 < N / 2) {
-          float v[32];
-          tc::tmem_ld32(tcol + (p & 1) * kN + cb * 32, v);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) fma2(acc[cb * 16 + e], v[2 * e], v[2 * e + 1], s2);
+      for (int j = 0; j < kN / 4; ++j) acc[j] = 0;
+      float s_next = __ldg(sp + min(gfirst, G - 1));
+      for (int p = 0; p < periods; ++p, ++pt) {
+        const float s = s_next;
+        if (!grid1 && p + 1 < periods) s_next = __ldg(sp + min(gfirst + p + 1, G - 1));
+        if (!warp_wait(&t_full[pt & 1], (pt >> 1) & 1, fail)) {
+          ok = false;
+          break;
         }
+        tc::fence_after_sync();
+        uint64_t s2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+#pragma unroll
+        for (int cb = 0; cb < kN / 32; ++cb) {
+          if (cb * 16 < N / 2) {
+            float v[16];
+            tc::tmem_ld16(tcol + (pt & 1) * kN + cb * 16, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) fma2(acc[cb * 8 + e], v[2 * e], v[2 * e + 1], s2);
+          }
+        }
+        tc::fence_before_sync();
+        warp_arrive(&t_empty[pt & 1]);
       }
-      tc::fence_before_sync();
-      tc::mbar_arrive(&t_empty[p & 1]);
-    }
-    auto store = [&](int64_t tok, int64_t rr, float v) {
-      if (tok < a.l.T && rr < a.l.m) {
-        if (a.l.xscale) v *= __ldg(a.l.xscale + tok);
+      if (!ok) {
+        if (lane == 0) record_status(a.hdr, GQ_ERR_TIMEOUT);
+      } else if (S == 1) {
+        const int cnt = (int)min((int64_t)(N / 2), a.l.T - tk);
+        const int rows = (int)min((int64_t)32, a.l.m - row0);
+        const float* xs = a.l.xscale ? a.l.xscale + tk : nullptr;
+        uint8_t* st = ostage + (warp - kScaleWarp) * kOutStage;
         if (a.l.y_bf16)
-          static_cast<__nv_bfloat16*>(a.l.y)[tok * a.l.m + rr] = __float2bfloat16(v);
+          store_tile(static_cast<__nv_bfloat16*>(a.l.y) + tk * a.l.m + row0, a.l.m, acc, cnt,
+                     rows, xs, wide, st, lane);
         else
-          static_cast<float*>(a.l.y)[tok * a.l.m + rr] = v;
-      }
-    };
-    if (!ok) {
-      if (lane == 0) record_status(a.hdr, GQ_ERR_TIMEOUT);
-    } else if (S == 1) {
+          store_tile(static_cast<float*>(a.l.y) + tk * a.l.m + row0, a.l.m, acc, cnt, rows, xs,
+                     wide, st, lane);
+      } else {
+        // partial sums as [token][row] over the operand rings (a shared tile is the CTA's only
+        // one, and every MMA of it is complete: its last accumulator has been read)
+        float* part = reinterpret_cast<float*>(base);
 #pragma unroll
-      for (int e = 0; e < kN / 4; ++e) {
-        if (2 * e < N / 2) {
-          const float2 v = *reinterpret_cast<const float2*>(&acc[e]);
-          store(t0 + half * (N / 2) + 2 * e, row, v.x);
-          store(t0 + half * (N / 2) + 2 * e + 1, row, v.y);
-        }
-      }
-    } else {
-      // partial sums as [token][row] over the operand rings (every MMA of this CTA is complete:
-      // its last accumulator has been read)
-      float* part = reinterpret_cast<float*>(base);
-#pragma unroll
-      for (int e = 0; e < kN / 4; ++e) {
-        if (2 * e < N / 2) {
-          const float2 v = *reinterpret_cast<const float2*>(&acc[e]);
-          float* q = part + (half * (N / 2) + 2 * e) * 128 + (warp & 3) * 32 + lane;
-          q[0] = v.x;
-          q[128] = v.y;
+        for (int e = 0; e < kN / 4; ++e) {
+          if (2 * e < N / 2) {
+            const float2 v = *reinterpret_cast<const float2*>(&acc[e]);
+            float* q = part + (half * (N / 2) + 2 * e) * 128 + quarter * 32 + lane;
+            q[0] = v.x;
+            q[128] = v.y;
+          }
         }
       }
     }
@@ -356,17 +473,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // Back to the launch's register share for the common end.  Only behind the barrier: the two
   // smaller shares may not grow before the larger one has been taken and given back, or it could
   // never be taken.
-  if constexpr (kN > 128) {
-    if (warp >= 8)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
-    else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
-  }
+  if (warp >= kScaleWarp)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 " GQ_LIN_REGS_LAUNCH ";");
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 " GQ_LIN_REGS_LAUNCH ";");
   if (warp == 1 && lane == 0) tc::mbar_wait(done, 0);  // also after a failure: no MMA in flight
   __syncwarp();
   if (S > 1) {
     cluster_sync();
     // this CTA adds the parts of its share of the tokens, in the order of the ranks
+    const int64_t row0 = (int64_t)(tile0 % a.mtiles) * 128, t0 = (int64_t)(tile0 / a.mtiles) * N;
     const uint32_t part = tc::smem_u32(base);
     const int n0 = (int)((int64_t)N * rank / S), n1 = (int)((int64_t)N * (rank + 1) / S);
     for (int i = n0 * 128 + tid; i < n1 * 128; i += kLinThreads) {
@@ -429,9 +545,11 @@ LinPlan plan_of(int64_t T, int64_t n, LinearInput kind, bool ordered) {
 }
 
 template <int B, int P, int kN>
-cudaError_t launch_tc(const CUtensorMap& map, const LinTcArgs& a, int vec, int S, cudaStream_t s) {
+cudaError_t launch_tc(const CUtensorMap& map, const LinTcArgs& a, int vec, int wide, int S,
+                      cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.mtiles * a.ntiles * S));
+  // one CTA an SM takes tile after tile, or S of them share one
+  cfg.gridDim = dim3((unsigned)(S > 1 ? a.tiles * S : a.tiles < kSMs ? a.tiles : kSMs));
   cfg.blockDim = dim3(kLinThreads);
   cfg.dynamicSmemBytes = kLinSmem;
   cfg.stream = s;
@@ -441,31 +559,31 @@ cudaError_t launch_tc(const CUtensorMap& map, const LinTcArgs& a, int vec, int S
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<B, P, kN>, map, a, vec);
+  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<B, P, kN>, map, a, vec, wide);
 }
 template <int B>
 cudaError_t launch_tc_bits(const CUtensorMap& map, const LinTcArgs& a, int P, int kN, int vec,
-                           int S, cudaStream_t s) {
-  if (P == 3) return launch_tc<B, 3, 128>(map, a, vec, S, s);
-  return kN == 128 ? launch_tc<B, 1, 128>(map, a, vec, S, s)
-                   : launch_tc<B, 1, 256>(map, a, vec, S, s);
+                           int wide, int S, cudaStream_t s) {
+  if (P == 3) return launch_tc<B, 3, 128>(map, a, vec, wide, S, s);
+  return kN == 128 ? launch_tc<B, 1, 128>(map, a, vec, wide, S, s)
+                   : launch_tc<B, 1, 256>(map, a, vec, wide, S, s);
+}
+template <int B, int P, int kN>
+cudaError_t init_one() {
+  cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<B, P, kN>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes at;
+  if ((e = cudaFuncGetAttributes(&at, linear_tc_kernel<B, P, kN>))) return e;
+  // the roles' register shares are what a launch of 96 registers a thread holds
+  return at.numRegs > 88 && at.numRegs <= 96 ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 template <int B>
 cudaError_t init_bits() {
   cudaError_t e;
-  cudaFuncAttributes at;
-  if ((e = cudaFuncSetAttribute(linear_tc_kernel<B, 3, 128>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem)))
-    return e;
-  if ((e = cudaFuncSetAttribute(linear_tc_kernel<B, 1, 128>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem)))
-    return e;
-  if ((e = cudaFuncSetAttribute(linear_tc_kernel<B, 1, 256>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinSmem)))
-    return e;
-  if ((e = cudaFuncGetAttributes(&at, linear_tc_kernel<B, 1, 256>))) return e;
-  // the warpgroups' register shares (40 + 112 + 2 x 176) have to fit the launch's registers
-  return at.numRegs >= 126 ? cudaSuccess : cudaErrorInvalidConfiguration;
+  if ((e = init_one<B, 3, 128>())) return e;
+  if ((e = init_one<B, 1, 128>())) return e;
+  return init_one<B, 1, 256>();
 }
 }  // namespace
 
@@ -520,11 +638,15 @@ cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaS
   t.ntiles = (int)((a.T + t.N - 1) / t.N);
   t.chunks = (int)((a.n + kChunk - 1) / kChunk);
   t.hdr = static_cast<WsHeader*>(ws);
+  t.gshift = a.group ? __builtin_ctz((unsigned)a.group) : 31;
+  t.dmask = a.group ? a.group / 16 - 1 : 15;
+  t.groups = a.group ? (int)((a.n + a.group - 1) / a.group) : 1;
   const int64_t tiles = (int64_t)t.mtiles * t.ntiles;
-  if (tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
+  if (tiles > INT32_MAX - kSMs) return cudaErrorInvalidValue;
+  t.tiles = (int)tiles;
   // columns shared by a cluster while tiles leave SMs idle and every CTA keeps four chunks
   int S = 1;
-  while (S < 8 && tiles * S * 2 <= 148 && t.chunks >= S * 8) S *= 2;
+  while (S < 8 && tiles * S * 2 <= kSMs && t.chunks >= S * 8) S *= 2;
   CUtensorMap map;
   cudaError_t e = encode_tmap_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, xt, rows_total, cols,
                                  ld, 64, (uint32_t)t.N, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -532,14 +654,15 @@ cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaS
   // widest loads of the packed words: rows start on 16-byte (8-byte) boundaries
   const int64_t words = row_words(a.n, a.bits);
   const int vec = words % 4 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 16 == 0;
+  const int wide = a.m * (a.y_bf16 ? 2 : 4) % 16 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
   switch (a.bits) {
-    case 2: e = launch_tc_bits<2>(map, t, p.P, kN, vec, S, s); break;
-    case 3: e = launch_tc_bits<3>(map, t, p.P, kN, vec, S, s); break;
-    case 4: e = launch_tc_bits<4>(map, t, p.P, kN, vec, S, s); break;
-    case 5: e = launch_tc_bits<5>(map, t, p.P, kN, vec, S, s); break;
-    case 6: e = launch_tc_bits<6>(map, t, p.P, kN, vec, S, s); break;
-    case 7: e = launch_tc_bits<7>(map, t, p.P, kN, vec, S, s); break;
-    default: e = launch_tc_bits<8>(map, t, p.P, kN, vec, S, s); break;
+    case 2: e = launch_tc_bits<2>(map, t, p.P, kN, vec, wide, S, s); break;
+    case 3: e = launch_tc_bits<3>(map, t, p.P, kN, vec, wide, S, s); break;
+    case 4: e = launch_tc_bits<4>(map, t, p.P, kN, vec, wide, S, s); break;
+    case 5: e = launch_tc_bits<5>(map, t, p.P, kN, vec, wide, S, s); break;
+    case 6: e = launch_tc_bits<6>(map, t, p.P, kN, vec, wide, S, s); break;
+    case 7: e = launch_tc_bits<7>(map, t, p.P, kN, vec, wide, S, s); break;
+    default: e = launch_tc_bits<8>(map, t, p.P, kN, vec, wide, S, s); break;
   }
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
