@@ -16,7 +16,9 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libgq.so")
 BUILD_DIR = os.path.join(ROOT, "_build", "libgq")
 SOURCES = ["gq_api.cu", "gq_hessian.cu", "gq_factor.cu", "gq_dgemm.cu", "gq_quant.cu", "gq_lazy_tc.cu",
-           "gq_noalloc.cu", "gq_huffman.cu", "gq_split.cu", "gq_linear.cu", "gq_linear_tc.cu", "gq_norm.cu"]
+           "gq_noalloc.cu", "gq_huffman.cu", "gq_split.cu", "gq_linear.cu", "gq_norm.cu"]
+# one source compiled once for every code width
+SOURCES += [("gq_linear_bits.cu", f"GQ_LINEAR_BITS={b}") for b in range(2, 9)]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -50,8 +52,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     cc = nvcc()
 
     def compile_one(src):
-        obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
-        cmd = [cc, *ARCH, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
+        src, define = src if isinstance(src, tuple) else (src, None)
+        name = src.replace(".cu", "" if define is None else "_" + define.split("=")[1])
+        obj = os.path.join(BUILD_DIR, name + ".o")
+        defs = [] if define is None else ["-D" + define]
+        cmd = [cc, *ARCH, *FLAGS, *extra_flags, *defs, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")

@@ -1,0 +1,439 @@
+// Products with a packed layer for few tokens: y[t][r] = sum_g s[r][g] sum_{k in g} x[t][k]
+// (c[r][k] - z[r][g]), the codes read as gq_quantize_layer wrote them.
+//
+// The bound for one token is the packed stream (m n b / 8 bytes); what has to be kept down beside
+// it is the work per weight of unpacking, and enough loads have to be in flight.  A warp
+// multiplies 16 rows with 8 tokens on mma.sync m16n8k16 (the tokens' dimension costs nothing up
+// to 8), operands straight from global memory in fragment order.  Any assignment of columns to
+// the instruction's k slots is right as long as both operands agree, so in a chunk of 128 columns
+// lane t of a quad takes columns 32 t .. 32 t + 31 of its two rows: b whole words of the stream, in
+// 16-byte loads where rows are aligned.  With groups of 64 two lanes of a quad hold one group and
+// two the other; the chunk is then multiplied twice, with the other half's inputs at zero.
+// Groups of 32 and 16 take units of 32 columns instead, 8 columns a lane.
+// c - z is an exact integer in 16 bits, the products are exact, and the fp32 sums of one group
+// are multiplied by the group's scale in fp32: no weight is rounded.  The warps of a CTA share
+// the columns in chunks of 128 and add their sums in a fixed order; every warp loads a chunk
+// ahead.
+//
+// fp32 tokens are taken as three bf16 parts (8 + 8 + 8 bits, exact), three products a weight;
+// 8-bit tokens as fp16 integers.
+#pragma once
+#include "gq_internal.cuh"
+#include "gq_unpack.cuh"
+
+namespace gq {
+
+namespace {
+template <bool kHalf>
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (kHalf)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The lane's eight codes of one unit: bits [8 t B, 8 (t + 1) B) of the unit's B words.
+template <int B>
+__device__ __forceinline__ void load_codes(const uint32_t* __restrict__ row, int unit, int t,
+                                           int words, uint32_t& lo, uint32_t& hi) {
+  const int w = unit * B + (t * B) / 4;
+  const uint32_t shift = 8 * ((t * B) % 4);
+  const uint32_t w0 = w < words ? __ldg(row + w) : 0u;
+  if constexpr (B == 4) {
+    lo = w0;
+    hi = 0;
+  } else if constexpr (B == 2) {
+    lo = w0 >> shift;
+    hi = 0;
+  } else {
+    const uint32_t w1 = w + 1 < words ? __ldg(row + w + 1) : 0u;
+    lo = __funnelshift_r(w0, w1, shift);
+    hi = w1 >> shift;
+    if constexpr (B == 7) {
+      const uint32_t w2 = w + 2 < words ? __ldg(row + w + 2) : 0u;
+      hi = __funnelshift_r(w1, w2, shift);
+    }
+  }
+}
+
+// Eight inputs x[k .. k+7] of one token as they lie in memory.
+template <LinearInput K>
+struct Raw {
+  uint32_t r[K == kXBf16 ? 4 : K == kXFp32 ? 8 : 2];
+};
+// fast: whole vectors, all eight columns inside the row.
+template <LinearInput K>
+__device__ __forceinline__ void load_raw(const void* xrow, int k, int n,
+                                         const int32_t* __restrict__ perm, bool fast, Raw<K>& o) {
+  constexpr int R = sizeof(o.r) / 4;
+  if (fast) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(
+        static_cast<const char*>(xrow) + (int64_t)k * (R / 2));
+    if constexpr (R == 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      o.r[0] = v.x; o.r[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < R / 4; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        o.r[4 * i] = v.x; o.r[4 * i + 1] = v.y; o.r[4 * i + 2] = v.z; o.r[4 * i + 3] = v.w;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) o.r[i] = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (k + i >= n) continue;
+    const int64_t at = perm ? perm_at(perm, k + i, n) : k + i;
+    if constexpr (K == kXBf16)
+      o.r[i >> 1] |= (uint32_t)__ldg(static_cast<const uint16_t*>(xrow) + at) << (16 * (i & 1));
+    else if constexpr (K == kXFp32)
+      o.r[i] = __ldg(static_cast<const uint32_t*>(xrow) + at);
+    else
+      o.r[i >> 2] |= (uint32_t)__ldg(static_cast<const uint8_t*>(xrow) + at) << (8 * (i & 3));
+  }
+}
+// The same as pairs (i, i + 4) of 16-bit floats, P parts each.
+template <LinearInput K, int P>
+__device__ __forceinline__ void input_pairs(const Raw<K>& x, uint32_t (&b)[P][4]) {
+  if constexpr (K == kXBf16) {
+    b[0][0] = __byte_perm(x.r[0], x.r[2], 0x5410);
+    b[0][1] = __byte_perm(x.r[0], x.r[2], 0x7632);
+    b[0][2] = __byte_perm(x.r[1], x.r[3], 0x5410);
+    b[0][3] = __byte_perm(x.r[1], x.r[3], 0x7632);
+  } else if constexpr (K == kXFp32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h0, m0, l0, h1, m1, l1;
+      split3(__uint_as_float(x.r[i]), h0, m0, l0);
+      split3(__uint_as_float(x.r[i + 4]), h1, m1, l1);
+      b[0][i] = __byte_perm(h0, h1, 0x7632);
+      b[1][i] = __byte_perm(m0, m1, 0x7632);
+      b[2][i] = __byte_perm(l0, l1, 0x7632);
+    }
+  } else {
+    // int8 -> fp16: 1024 + (v + 128), minus 1152
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t p = __byte_perm(x.r[0], x.r[1], 0x0400 + 0x0101 * i);
+      b[0][i] = f16x2_sub((p & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
+    }
+  }
+}
+
+template <LinearInput K>
+__device__ __forceinline__ const void* token_row(const void* x, int64_t t, int64_t n) {
+  constexpr int size = K == kXBf16 ? 2 : K == kXFp32 ? 4 : 1;
+  return static_cast<const char*>(x) + t * n * size;
+}
+
+// B consecutive words of a row from word w0 on (0 behind the row's end).
+template <int B>
+__device__ __forceinline__ void load_run(const uint32_t* __restrict__ row, int w0, int words,
+                                         bool vec, uint32_t (&w)[B]) {
+  if (vec && w0 + B <= words) {
+    if constexpr (B % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < B / 4; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + w0) + i);
+        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+      }
+      return;
+    } else if constexpr (B % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < B / 2; ++i) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + w0) + i);
+        w[2 * i] = v.x; w[2 * i + 1] = v.y;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < B; ++i) w[i] = w0 + i < words ? __ldg(row + w0 + i) : 0u;
+}
+
+// One warp's share of a chunk of 128 columns for a lane's 2 RT rows, and of one token's inputs.
+template <int B, LinearInput K, int RT>
+struct Chunk {
+  uint32_t w[2 * RT][B];  // lane t's 32 columns
+  uint32_t z[2 * RT];     // their zero points
+  float f[2 * RT][2];     // scales of the chunk's group, or of its halves'
+  Raw<K> x[4];
+};
+// How a chunk's columns fall into groups: one group or more of 128 columns, halves of 64, or units
+// of 32 and 16.
+enum GroupMode { kWhole = 0, kHalves = 1, kFine = 2 };
+}  // namespace
+
+// One CTA: 16 RT rows x (8 NT) tokens.  gshift: log2 of the group width (31: one grid per row).
+// xvec, cvec: inputs and packed rows allow wide loads.
+template <int B, LinearInput K, int NT, int RT, GroupMode M, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32)
+    linear_rows_kernel(LinearArgs a, int gshift, int G, int xvec, int cvec) {
+  constexpr bool kHalf = K == kXInt8;
+  constexpr int P = K == kXFp32 ? 3 : 1;
+  constexpr int kRows = 16 * RT;
+  __shared__ float red[kWarps][NT * 8][kRows + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t row0 = (int64_t)blockIdx.x * kRows;
+  const int n = (int)a.n, words = (int)row_words(a.n, B), chunks = (n + 127) / 128;
+  const uint32_t* cp[2 * RT];  // the lane's rows: g, g + 8 of every tile of 16
+  const float* sp[2 * RT];
+  const uint8_t* zp[2 * RT];
+#pragma unroll
+  for (int r = 0; r < 2 * RT; ++r) {
+    const int64_t row = min(row0 + 8 * r + g, a.m - 1);
+    cp[r] = a.codes + row * words;
+    sp[r] = a.scales + row * G;
+    zp[r] = a.zeros + row * G;
+  }
+
+  for (int64_t t0 = (int64_t)blockIdx.y * NT * 8; t0 < a.T; t0 += (int64_t)gridDim.y * NT * 8) {
+    float acc[RT][NT][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][j][i] = 0.f;
+    // (behind the last token its row again: a column of the product is one token's alone, and
+    // these columns are not stored)
+    const void* xrow[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) xrow[j] = token_row<K>(a.x, min(t0 + j * 8 + g, a.T - 1), a.n);
+
+    if constexpr (M != kFine) {
+      auto fetch = [&](int c, Chunk<B, K, RT>& q) {
+        const bool fast = xvec && c * 128 + 128 <= n;
+        if constexpr (NT == 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            load_raw<K>(xrow[0], c * 128 + 32 * t + 8 * i, n, a.perm, fast, q.x[i]);
+        }
+        const int gl = min((c * 128 + 32 * t) >> gshift, G - 1);
+        const int g0 = min((c * 128) >> gshift, G - 1);
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) {
+          load_run<B>(cp[r], (c * 4 + t) * B, words, cvec, q.w[r]);
+          q.z[r] = __ldg(zp[r] + gl);
+          q.f[r][0] = __ldg(sp[r] + g0);
+          if constexpr (M == kHalves) q.f[r][1] = __ldg(sp[r] + min(g0 + 1, G - 1));
+        }
+      };
+      auto multiply = [&](int c, const Chunk<B, K, RT>& q) {
+        const bool fast = xvec && c * 128 + 128 <= n;
+        constexpr int kSets = M == kHalves ? 2 : 1;
+        uint32_t zz[2 * RT];
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) zz[r] = zero_pair<B, kHalf>(q.z[r]);
+        float part[kSets][RT][NT][4];
+#pragma unroll
+        for (int h = 0; h < kSets; ++h)
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) part[h][r][j][i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // eight columns of the lane
+          constexpr int kTop = B - 1;
+          const int w = (i * B) / 4, sh = 8 * ((i * B) % 4);
+          const int w1 = w + 1 < B ? w + 1 : kTop, w2 = w + 2 < B ? w + 2 : kTop;
+          uint32_t pr[2 * RT][4];
+#pragma unroll
+          for (int r = 0; r < 2 * RT; ++r) {
+            code_pairs<B>(__funnelshift_r(q.w[r][w], q.w[r][w1], sh),
+                          __funnelshift_r(q.w[r][w1], q.w[r][w2], sh), pr[r]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pr[r][e] = pair_value<B, kHalf>(pr[r][e], zz[r]);
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            uint32_t b[P][4];
+            if constexpr (NT == 1) {
+              input_pairs<K, P>(q.x[i], b);
+            } else {
+              Raw<K> x;
+              load_raw<K>(xrow[j], c * 128 + 32 * t + 8 * i, n, a.perm, fast, x);
+              input_pairs<K, P>(x, b);
+            }
+#pragma unroll
+            for (int h = 0; h < kSets; ++h) {
+              const bool mine = M == kWhole || (t >> 1) == h;
+#pragma unroll
+              for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                  const uint32_t b0 = mine ? b[p][e] : 0u, b1 = mine ? b[p][e + 1] : 0u;
+#pragma unroll
+                  for (int r = 0; r < RT; ++r)
+                    mma_16816<kHalf>(part[h][r][j], pr[2 * r][e], pr[2 * r + 1][e],
+                                     pr[2 * r][e + 1], pr[2 * r + 1][e + 1], b0, b1);
+                }
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < kSets; ++h)
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[r][j][i] += q.f[2 * r + (i >> 1)][h] * part[h][r][j][i];
+      };
+      Chunk<B, K, RT> q0, q1;
+      int c = warp;
+      if (c < chunks) fetch(c, q0);
+      while (c < chunks) {
+        if (c + kWarps < chunks) fetch(c + kWarps, q1);
+        multiply(c, q0);
+        c += kWarps;
+        if (c >= chunks) break;
+        if (c + kWarps < chunks) fetch(c + kWarps, q0);
+        multiply(c, q1);
+        c += kWarps;
+      }
+    } else {
+      const bool g16 = gshift == 4;
+      for (int u0 = warp * 4; u0 < chunks * 4; u0 += kWarps * 4) {
+        const bool fast = xvec && u0 * 32 + 128 <= n;
+        uint32_t w[2 * RT][4][2], z[2 * RT][4];
+        float f[2 * RT][4];
+        Raw<K> x1[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int unit = u0 + u;
+          if constexpr (NT == 1) load_raw<K>(xrow[0], unit * 32 + 8 * t, n, a.perm, fast, x1[u]);
+          const int gl = min((unit * 32 + 8 * t) >> gshift, G - 1);
+          const int g0 = min((unit * 32) >> gshift, G - 1);
+#pragma unroll
+          for (int r = 0; r < 2 * RT; ++r) {
+            load_codes<B>(cp[r], unit, t, words, w[r][u][0], w[r][u][1]);
+            z[r][u] = __ldg(zp[r] + gl);
+            f[r][u] = __ldg(sp[r] + g0);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int unit = u0 + u;
+          uint32_t pr[2 * RT][4];
+          float f1[2 * RT];
+#pragma unroll
+          for (int r = 0; r < 2 * RT; ++r) {
+            code_pairs<B>(w[r][u][0], w[r][u][1], pr[r]);
+            const uint32_t zz = zero_pair<B, kHalf>(z[r][u]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pr[r][i] = pair_value<B, kHalf>(pr[r][i], zz);
+            f1[r] = g16 ? __ldg(sp[r] + min(unit * 2 + 1, G - 1)) : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            uint32_t b[P][4];
+            if constexpr (NT == 1) {
+              input_pairs<K, P>(x1[u], b);
+            } else {
+              Raw<K> x;
+              load_raw<K>(xrow[j], unit * 32 + 8 * t, n, a.perm, fast, x);
+              input_pairs<K, P>(x, b);
+            }
+            // groups of 16: lanes 0, 1 of a quad hold the unit's first group, lanes 2, 3 its
+            // second; each half is multiplied with the other half's inputs at zero
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h == 1 && !g16) break;
+              const bool mine = !g16 || (t >> 1) == h;
+#pragma unroll
+              for (int r = 0; r < RT; ++r) {
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                  for (int e = 0; e < 4; e += 2)
+                    mma_16816<kHalf>(c, pr[2 * r][e], pr[2 * r + 1][e], pr[2 * r][e + 1],
+                                     pr[2 * r + 1][e + 1], mine ? b[p][e] : 0u,
+                                     mine ? b[p][e + 1] : 0u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  acc[r][j][i] += (h ? f1[2 * r + (i >> 1)] : f[2 * r + (i >> 1)][u]) * c[i];
+              }
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          red[warp][j * 8 + 2 * t + (i & 1)][16 * r + g + 8 * (i >> 1)] = acc[r][j][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < NT * 8 * kRows; i += kWarps * 32) {
+      const int tt = i / kRows, rr = i % kRows;
+      const int64_t tok = t0 + tt, row = row0 + rr;
+      if (tok < a.T && row < a.m) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += red[w][tt][rr];
+        if constexpr (K == kXInt8) v *= a.xscale[tok];
+        if (a.y_bf16)
+          static_cast<__nv_bfloat16*>(a.y)[tok * a.m + row] = __float2bfloat16(v);
+        else
+          static_cast<float*>(a.y)[tok * a.m + row] = v;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+namespace {
+template <int B, LinearInput K, GroupMode M>
+void launch_mode(const LinearArgs& a, int xvec, cudaStream_t s) {
+  const int gshift = a.group ? __builtin_ctz((unsigned)a.group) : 31;
+  const int G = a.group ? (int)((a.n + a.group - 1) / a.group) : 1;
+  const int cvec = row_words(a.n, B) % 4 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 16 == 0;
+  auto grid = [&](int rows, int tokens) {
+    const int64_t tiles = (a.T + tokens - 1) / tokens;
+    return dim3((unsigned)((a.m + rows - 1) / rows), (unsigned)(tiles < 32768 ? tiles : 32768));
+  };
+  // two tiles of rows a warp share the inputs' part of the work; with few rows one tile leaves
+  // more CTAs for the SMs
+  const bool two = a.m >= 2048;
+  if (a.T <= 8 && !two)
+    linear_rows_kernel<B, K, 1, 1, M, 8><<<grid(16, 8), 256, 0, s>>>(a, gshift, G, xvec, cvec);
+  else if (a.T <= 8)
+    linear_rows_kernel<B, K, 1, 2, M, 16><<<grid(32, 8), 512, 0, s>>>(a, gshift, G, xvec, cvec);
+  else if (a.T <= 16)
+    linear_rows_kernel<B, K, 2, 2, M, 8><<<grid(32, 16), 256, 0, s>>>(a, gshift, G, xvec, cvec);
+  else
+    linear_rows_kernel<B, K, 4, 1, M, 8><<<grid(16, 32), 256, 0, s>>>(a, gshift, G, xvec, cvec);
+}
+template <int B, LinearInput K>
+void launch_input(const LinearArgs& a, int xvec, cudaStream_t s) {
+  if (a.group == 16 || a.group == 32) launch_mode<B, K, kFine>(a, xvec, s);
+  else if (a.group == 64) launch_mode<B, K, kHalves>(a, xvec, s);
+  else launch_mode<B, K, kWhole>(a, xvec, s);
+}
+}  // namespace
+
+template <int B>
+void linear_rows_bits(const LinearArgs& a, LinearInput kind, int xvec, cudaStream_t s) {
+  if (kind == kXBf16) launch_input<B, kXBf16>(a, xvec, s);
+  else if (kind == kXFp32) launch_input<B, kXFp32>(a, xvec, s);
+  else launch_input<B, kXInt8>(a, xvec, s);
+}
+
+}  // namespace gq

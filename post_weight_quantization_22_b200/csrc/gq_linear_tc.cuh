@@ -19,7 +19,9 @@
 //
 // Roles: warp 0 the tokens' TMA loads, warp 1 the MMAs, warps 4-11 unpack (four for the even
 // stages of the ring, four for the odd ones), warps 12-19 scale and add.
+#pragma once
 #include "gq_internal.cuh"
+#include "gq_linear.cuh"
 #include "gq_tc.cuh"
 #include "gq_unpack.cuh"
 
@@ -34,8 +36,6 @@ constexpr int kUnpackWarp = 4, kScaleWarp = 12;   // first warps of these roles,
 #define GQ_LIN_REGS_UNPACK "48"
 #define GQ_LIN_REGS_SCALE "176"
 #define GQ_LIN_REGS_LAUNCH "96"
-constexpr int kSMs = 148;
-constexpr int kCols = 64;                         // columns per stage of the ring
 constexpr uint32_t kTile = 128 * kCols * 2;       // 128 rows or tokens of them, 128 bytes each
 constexpr uint32_t kOutStage = 1024;              // a scaling warp's output staging
 // Shared memory: the ring of stages (each the unpacked rows and P parts of the tokens), the
@@ -48,18 +48,6 @@ constexpr int lin_chunks(int B, int P) {
   return fit < 8 ? fit : 8;
 }
 
-struct LinTcArgs {
-  LinearArgs l;
-  int planes_t;      // rows between two parts of the tokens (0 with one part)
-  int N;             // tokens per tile
-  int mtiles;        // tiles of 128 rows (pairs: 256)
-  int tiles;         // tiles of rows and tokens
-  int stages;        // stages of kCols columns
-  int gshift;        // log2 of the group width (31: one grid per row, every index is 0)
-  int dmask;         // 16-column steps per accumulator period (a power of two) - 1
-  int groups;        // groups of a row
-  WsHeader* hdr;
-};
 
 // Waits as mbar_wait (acquire at cluster scope), but also gives up when another role of the CTA
 // has.
@@ -653,47 +641,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
 }
 
-// ---- tokens as bf16 parts: P x T rows of ld elements, columns behind n zero ----
-template <LinearInput K>
-__global__ void linear_stage_kernel(const void* __restrict__ x, int64_t T, int64_t n, int64_t ld,
-                                    const int32_t* __restrict__ perm, uint16_t* __restrict__ out) {
-  const int64_t t = blockIdx.x;
-  for (int64_t k = threadIdx.x; k < ld; k += blockDim.x) {
-    const int64_t src = t * n + (k < n ? (perm ? perm_at(perm, k, n) : k) : 0);
-    uint16_t* o = out + t * ld + k;
-    if constexpr (K == kXFp32) {
-      const float v = k < n ? static_cast<const float*>(x)[src] : 0.f;
-      uint32_t h, m, l;
-      split3(v, h, m, l);
-      o[0] = (uint16_t)(h >> 16);
-      o[T * ld] = (uint16_t)(m >> 16);
-      o[2 * T * ld] = (uint16_t)(l >> 16);
-    } else if constexpr (K == kXInt8) {
-      const float v = k < n ? (float)static_cast<const int8_t*>(x)[src] : 0.f;
-      o[0] = __bfloat16_as_ushort(__float2bfloat16(v));
-    } else {
-      o[0] = k < n ? static_cast<const uint16_t*>(x)[src] : (uint16_t)0;
-    }
-  }
-}
-
 namespace {
-// What a call does: whether the tokens are staged, the tile and the split of the columns.
-struct LinPlan {
-  bool tc, staged;
-  int P;
-  int64_t ld;      // staged row length, elements
-};
-LinPlan plan_of(int64_t T, int64_t n, LinearInput kind, bool ordered) {
-  LinPlan p{};
-  p.tc = T > 32;
-  p.P = kind == kXFp32 ? 3 : 1;
-  // TMA takes rows whose length is a multiple of 16 bytes
-  p.staged = kind != kXBf16 || ordered || n % 8 != 0;
-  p.ld = (n + 63) / 64 * 64;
-  return p;
-}
-
 template <int B, int P, bool kPair>
 cudaError_t launch_tc(const CUtensorMap& map, const CUtensorMap& cmap, const LinTcArgs& a, int vec,
                       int wide, int S, cudaStream_t s) {
@@ -713,8 +661,10 @@ cudaError_t launch_tc(const CUtensorMap& map, const CUtensorMap& cmap, const Lin
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, linear_tc_kernel<B, P, kPair>, map, cmap, a, vec, wide);
 }
+}  // namespace
+
 template <int B>
-cudaError_t launch_tc_bits(const CUtensorMap& map, const LinTcArgs& a, int P, bool pair, int vec,
+cudaError_t linear_tc_bits(const CUtensorMap& map, const LinTcArgs& a, int P, bool pair, int vec,
                            int wide, int S, cudaStream_t s) {
   CUtensorMap cmap = map;  // the packed rows (pairs)
   if (pair) {
@@ -731,6 +681,7 @@ cudaError_t launch_tc_bits(const CUtensorMap& map, const LinTcArgs& a, int P, bo
   return pair ? launch_tc<B, 1, true>(map, cmap, a, vec, wide, S, s)
               : launch_tc<B, 1, false>(map, cmap, a, vec, wide, S, s);
 }
+namespace {
 template <int B, int P, bool kPair>
 cudaError_t init_one() {
   cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<B, P, kPair>,
@@ -741,97 +692,16 @@ cudaError_t init_one() {
   // the roles' register shares are what a launch of 96 registers a thread holds
   return at.numRegs > 88 && at.numRegs <= 96 ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
+}  // namespace
+
 template <int B>
-cudaError_t init_bits() {
+cudaError_t linear_tc_init() {
   cudaError_t e;
   if ((e = init_one<B, 3, false>())) return e;
   if ((e = init_one<B, 3, true>())) return e;
   if ((e = init_one<B, 1, false>())) return e;
   return init_one<B, 1, true>();
 }
-}  // namespace
 
-size_t linear_ws_bytes(int64_t T, int64_t n, LinearInput kind, bool ordered) {
-  const LinPlan p = plan_of(T, n, kind, ordered);
-  if (!p.tc) return 0;
-  return kAlign + (p.staged ? align_up((size_t)p.P * T * p.ld * 2) : 0);
-}
-
-cudaError_t linear_init_attributes() {
-  cudaError_t e;
-  if ((e = init_bits<2>())) return e;
-  if ((e = init_bits<3>())) return e;
-  if ((e = init_bits<4>())) return e;
-  if ((e = init_bits<5>())) return e;
-  if ((e = init_bits<6>())) return e;
-  if ((e = init_bits<7>())) return e;
-  return init_bits<8>();
-}
-
-cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaStream_t s) {
-  if (a.T == 0) return cudaSuccess;
-  const LinPlan p = plan_of(a.T, a.n, kind, a.perm != nullptr);
-  // a misaligned matrix cannot be a tensor map: the warp-level kernel reads it in place
-  const bool aligned = p.staged || reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
-  const int64_t rows_total = (int64_t)p.P * a.T;
-  if (!p.tc || !aligned || rows_total > INT32_MAX) return launch_linear_rows(a, kind, s);
-  const void* xt = a.x;
-  int64_t ld = a.n, cols = a.n;
-  if (p.staged) {
-    uint16_t* out = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kAlign);
-    const unsigned grid = (unsigned)a.T;
-    if (kind == kXFp32)
-      linear_stage_kernel<kXFp32><<<grid, 256, 0, s>>>(a.x, a.T, a.n, p.ld, a.perm, out);
-    else if (kind == kXInt8)
-      linear_stage_kernel<kXInt8><<<grid, 256, 0, s>>>(a.x, a.T, a.n, p.ld, a.perm, out);
-    else
-      linear_stage_kernel<kXBf16><<<grid, 256, 0, s>>>(a.x, a.T, a.n, p.ld, a.perm, out);
-    count_launches(1);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    xt = out;
-    ld = cols = p.ld;
-  }
-  LinTcArgs t{};
-  t.l = a;
-  t.l.perm = nullptr;
-  t.planes_t = p.P > 1 ? (int)a.T : 0;
-  // widest loads of the packed words: rows start on 16-byte boundaries
-  const int64_t words = row_words(a.n, a.bits);
-  const int vec = words % 4 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 16 == 0;
-  // pairs of CTAs where their 256 x 256 tiles occupy the SMs, and the packed rows can be a
-  // tensor map
-  const int64_t pairs = ((a.m + 255) / 256) * ((a.T + 255) / 256);
-  const bool pair = vec && pairs >= kSMs / 4;
-  t.N = pair ? 256 : a.T >= 128 ? 128 : (int)(a.T + 63) / 64 * 64;
-  t.mtiles = (int)((a.m + (pair ? 255 : 127)) / (pair ? 256 : 128));
-  const int64_t tiles = t.mtiles * ((a.T + t.N - 1) / t.N);
-  t.stages = (int)((a.n + kCols - 1) / kCols);
-  t.hdr = static_cast<WsHeader*>(ws);
-  t.gshift = a.group ? __builtin_ctz((unsigned)a.group) : 31;
-  t.dmask = a.group ? a.group / 16 - 1 : 15;
-  t.groups = a.group ? (int)((a.n + a.group - 1) / a.group) : 1;
-  if (tiles > INT32_MAX - kSMs) return cudaErrorInvalidValue;
-  t.tiles = (int)tiles;
-  // columns shared by a cluster while tiles leave SMs idle and every CTA keeps eight stages
-  int S = 1;
-  while (!pair && S < 8 && tiles * S * 2 <= kSMs && t.stages >= S * 16) S *= 2;
-  CUtensorMap map;
-  cudaError_t e = encode_tmap_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, xt, rows_total, cols,
-                                 ld, kCols, (uint32_t)(pair ? 128 : t.N), CU_TENSOR_MAP_SWIZZLE_128B);
-  if (e != cudaSuccess) return e;
-  const int wide = a.m * (a.y_bf16 ? 2 : 4) % 16 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
-  switch (a.bits) {
-    case 2: e = launch_tc_bits<2>(map, t, p.P, pair, vec, wide, S, s); break;
-    case 3: e = launch_tc_bits<3>(map, t, p.P, pair, vec, wide, S, s); break;
-    case 4: e = launch_tc_bits<4>(map, t, p.P, pair, vec, wide, S, s); break;
-    case 5: e = launch_tc_bits<5>(map, t, p.P, pair, vec, wide, S, s); break;
-    case 6: e = launch_tc_bits<6>(map, t, p.P, pair, vec, wide, S, s); break;
-    case 7: e = launch_tc_bits<7>(map, t, p.P, pair, vec, wide, S, s); break;
-    default: e = launch_tc_bits<8>(map, t, p.P, pair, vec, wide, S, s); break;
-  }
-  count_launches(1);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
 
 }  // namespace gq

@@ -9,6 +9,7 @@ module without it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -424,54 +425,60 @@ def gq_huffman_encode(codes: torch.Tensor, stream_words: int | None = None, ws=N
 # running a quantized layer
 # ---------------------------------------------------------------------------------------------
 # These calls run on the tensors' device, whichever is current, and on ``stream`` (default: that
-# device's current stream); what they allocate is allocated on that stream.
+# device's current stream); what they allocate is allocated on that stream.  A call on one token
+# takes the GPU a few microseconds, so the checks here are kept to what a few comparisons can say.
+
+def _elsewhere(device: int, stream) -> bool:
+    return stream is not None or device != torch.cuda.current_device()
+
 
 class _On:
-    """The tensors' device and the call's stream made current (only where they are not)."""
+    """The tensors' device and the call's stream made current."""
 
-    def __init__(self, dev, stream):
-        self.ctx = []
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-            self.ctx.append(torch.cuda.stream(stream))
-        elif dev.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(dev))
+    def __init__(self, device: int, stream):
+        if stream is not None and stream.device.index != device:
+            raise ValueError(f"stream on {stream.device}, tensors on cuda:{device}")
+        self.ctx = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
+        self.ctx.__enter__()
 
     def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+        return self.ctx.__exit__(*exc)
 
 
-def _need_on(t, dtype, shape, dev, name):
-    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dev} {dtype} {tuple(shape)}, got "
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, by device index
+
+
+def _need_on(t, dtype, shape, device, name):
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != device
+            or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected contiguous cuda:{device} {dtype} {tuple(shape)}, got "
                          f"{t.device} {t.dtype} {tuple(t.shape)}")
 
 
 def _rows(x, name):
-    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+    device = x.get_device()
+    if x.dim() != 2 or device < 0 or not x.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous cuda matrix (tokens x features), got "
                          f"{x.device} {tuple(x.shape)}")
-    return x.shape
+    return x.shape, device
 
 
-def _layer_args(codes, scales, zeros, n, bits, group_size, perm, dev):
+def _layer_args(codes, scales, zeros, n, bits, group_size, perm, device):
     if not 2 <= bits <= 8:
         raise ValueError(f"bits: 2 to 8, got {bits}")
+    if group_size < 0:
+        raise ValueError(f"group_size: 0 or a group width, got {group_size}")
     if codes.dim() != 2:
         raise ValueError("codes: expected rows of packed words")
     m = codes.shape[0]
-    G = 1 if group_size == 0 else -(-n // group_size)
-    _need_on(codes, torch.int32, (m, (n * bits + 31) // 32), dev, "codes")
-    _need_on(scales, torch.float32, (m, G), dev, "scales")
-    _need_on(zeros, torch.uint8, (m, G), dev, "zeros")
+    grid = (m, 1 if group_size == 0 else -(-n // group_size))
+    _need_on(codes, torch.int32, (m, (n * bits + 31) // 32), device, "codes")
+    _need_on(scales, torch.float32, grid, device, "scales")
+    _need_on(zeros, torch.uint8, grid, device, "zeros")
     if perm is not None:
-        _need_on(perm, torch.int32, (n,), dev, "perm")
+        _need_on(perm, torch.int32, (n,), device, "perm")
     return m
 
 
@@ -481,24 +488,31 @@ def gq_order_codes(codes: torch.Tensor, n: int, bits: int, perm: torch.Tensor, o
     processing order: once per layer, for gq_linear / gq_linear_quantized with the same perm."""
     if not 2 <= bits <= 8:
         raise ValueError(f"bits: 2 to 8, got {bits}")
-    m, _ = _rows(codes, "codes")
-    dev = codes.device
-    _need_on(codes, torch.int32, (m, n_words(n, bits)), dev, "codes")
-    _need_on(perm, torch.int32, (n,), dev, "perm")
-    with _On(dev, stream):
-        out = torch.empty_like(codes) if out is None else out
-        _need_on(out, torch.int32, codes.shape, dev, "out")
-        _check(LIB.gq_order_codes(codes.data_ptr(), m, n, bits, perm.data_ptr(), out.data_ptr(),
-                                  torch.cuda.current_stream(dev).cuda_stream), "gq_order_codes")
+    (m, _), device = _rows(codes, "codes")
+    if _elsewhere(device, stream):
+        with _On(device, stream):
+            return gq_order_codes(codes, n, bits, perm, out)
+    _need_on(codes, torch.int32, (m, n_words(n, bits)), device, "codes")
+    _need_on(perm, torch.int32, (n,), device, "perm")
+    out = torch.empty_like(codes) if out is None else out
+    _need_on(out, torch.int32, codes.shape, device, "out")
+    _check(LIB.gq_order_codes(codes.data_ptr(), m, n, bits, perm.data_ptr(), out.data_ptr(),
+                              _raw_stream(device)), "gq_order_codes")
     return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_need(T, m, n, xc, ordered):
+    """Workspace bytes of a product (xc: a gq_dtype, or -1 for 8-bit rows)."""
+    if xc < 0:
+        return int(LIB.gq_linear_quantized_workspace_size(T, m, n, ordered))
+    return int(LIB.gq_linear_workspace_size(T, m, n, xc, ordered))
 
 
 def gq_linear_workspace_size(T: int, m: int, n: int, x_dtype=torch.bfloat16,
                              ordered: bool = False) -> int:
-    if x_dtype == torch.int8:
-        return int(LIB.gq_linear_quantized_workspace_size(T, m, n, int(bool(ordered))))
-    code = GQ_BF16 if x_dtype == torch.bfloat16 else GQ_FP32
-    return int(LIB.gq_linear_workspace_size(T, m, n, code, int(bool(ordered))))
+    code = {torch.int8: -1, torch.bfloat16: GQ_BF16, torch.float32: GQ_FP32}[x_dtype]
+    return _linear_need(T, m, n, code, bool(ordered))
 
 
 def gq_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
@@ -506,24 +520,24 @@ def gq_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros:
               stream=None) -> torch.Tensor:
     """y = x W^T (T x m) with a packed layer (gq_quantize_layer); x T x n in bf16 or fp32, y in
     ``y_dtype`` (default: x's).  ``perm``: the codes are in processing order (gq_order_codes)."""
-    T, n = _rows(x, "x")
-    dev = x.device
+    (T, n), device = _rows(x, "x")
+    if _elsewhere(device, stream):
+        with _On(device, stream):
+            return gq_linear(x, codes, scales, zeros, bits, group_size, perm, y, y_dtype, ws)
     xc = _dtype_code(x)
-    m = _layer_args(codes, scales, zeros, n, bits, group_size, perm, dev)
-    with _On(dev, stream):
-        if y is None:
-            y = torch.empty((T, m), dtype=x.dtype if y_dtype is None else y_dtype, device=dev)
-        yc = _dtype_code(y)
-        _need_on(y, y.dtype, (T, m), dev, "y")
-        if ws is None:
-            need = LIB.gq_linear_workspace_size(T, m, n, xc, int(perm is not None))
-            ws = workspace(need, dev) if need else None
-        _check(LIB.gq_linear(x.data_ptr(), xc, T, m, n, codes.data_ptr(), scales.data_ptr(),
-                             zeros.data_ptr(), bits, group_size,
-                             None if perm is None else perm.data_ptr(), y.data_ptr(), yc,
-                             None if ws is None else ws.data_ptr(),
-                             0 if ws is None else ws.numel(),
-                             torch.cuda.current_stream(dev).cuda_stream), "gq_linear")
+    m = _layer_args(codes, scales, zeros, n, bits, group_size, perm, device)
+    if y is None:
+        y = torch.empty((T, m), dtype=x.dtype if y_dtype is None else y_dtype, device=x.device)
+    yc = _dtype_code(y)
+    _need_on(y, y.dtype, (T, m), device, "y")
+    if ws is None:
+        need = _linear_need(T, m, n, xc, perm is not None)
+        ws = workspace(need, x.device) if need else None
+    _check(LIB.gq_linear(x.data_ptr(), xc, T, m, n, codes.data_ptr(), scales.data_ptr(),
+                         zeros.data_ptr(), bits, group_size,
+                         None if perm is None else perm.data_ptr(), y.data_ptr(), yc,
+                         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                         _raw_stream(device)), "gq_linear")
     return y
 
 
@@ -532,25 +546,26 @@ def gq_linear_quantized(q: torch.Tensor, qscale: torch.Tensor, codes: torch.Tens
                         group_size: int = 0, perm=None, y=None, y_dtype=torch.bfloat16, ws=None,
                         stream=None) -> torch.Tensor:
     """gq_linear on 8-bit rows: x = qscale[:, None] * q (q int8 T x n, qscale fp32 T)."""
-    T, n = _rows(q, "q")
-    dev = q.device
-    _need_on(q, torch.int8, (T, n), dev, "q")
-    _need_on(qscale, torch.float32, (T,), dev, "qscale")
-    m = _layer_args(codes, scales, zeros, n, bits, group_size, perm, dev)
-    with _On(dev, stream):
-        if y is None:
-            y = torch.empty((T, m), dtype=y_dtype, device=dev)
-        yc = _dtype_code(y)
-        _need_on(y, y.dtype, (T, m), dev, "y")
-        if ws is None:
-            need = LIB.gq_linear_quantized_workspace_size(T, m, n, int(perm is not None))
-            ws = workspace(need, dev) if need else None
-        _check(LIB.gq_linear_quantized(
-            q.data_ptr(), qscale.data_ptr(), T, m, n, codes.data_ptr(), scales.data_ptr(),
-            zeros.data_ptr(), bits, group_size, None if perm is None else perm.data_ptr(),
-            y.data_ptr(), yc, None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel(),
-            torch.cuda.current_stream(dev).cuda_stream), "gq_linear_quantized")
+    (T, n), device = _rows(q, "q")
+    if _elsewhere(device, stream):
+        with _On(device, stream):
+            return gq_linear_quantized(q, qscale, codes, scales, zeros, bits, group_size, perm, y,
+                                       y_dtype, ws)
+    _need_on(q, torch.int8, (T, n), device, "q")
+    _need_on(qscale, torch.float32, (T,), device, "qscale")
+    m = _layer_args(codes, scales, zeros, n, bits, group_size, perm, device)
+    if y is None:
+        y = torch.empty((T, m), dtype=y_dtype, device=q.device)
+    yc = _dtype_code(y)
+    _need_on(y, y.dtype, (T, m), device, "y")
+    if ws is None:
+        need = _linear_need(T, m, n, -1, perm is not None)
+        ws = workspace(need, q.device) if need else None
+    _check(LIB.gq_linear_quantized(
+        q.data_ptr(), qscale.data_ptr(), T, m, n, codes.data_ptr(), scales.data_ptr(),
+        zeros.data_ptr(), bits, group_size, None if perm is None else perm.data_ptr(),
+        y.data_ptr(), yc, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+        _raw_stream(device)), "gq_linear_quantized")
     return y
 
 
@@ -560,31 +575,32 @@ def gq_rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
     rows q with qscale.  ``sum`` (h) is stored with a residual, or where a tensor is given; y only
     where a tensor is given; q unless y alone is given.  Returns dict(sum, y, q, qscale), None
     where not written."""
-    T, n = _rows(x, "x")
-    dev = x.device
-    xc, gc = _dtype_code(x), _dtype_code(gamma)
-    _need_on(gamma, gamma.dtype, (n,), dev, "gamma")
+    (T, n), device = _rows(x, "x")
+    if _elsewhere(device, stream):
+        with _On(device, stream):
+            return gq_rmsnorm_quantize(x, gamma, eps, residual, sum, y, q, qscale)
+    xc, gc, xt, shape = _dtype_code(x), _dtype_code(gamma), x.dtype, (T, n)
+    _need_on(gamma, gamma.dtype, (n,), device, "gamma")
     if (q is None) != (qscale is None):
         raise ValueError("q and qscale go together")
-    with _On(dev, stream):
-        if residual is not None:
-            _need_on(residual, x.dtype, (T, n), dev, "residual")
-            sum = torch.empty_like(x) if sum is None else sum
-        if q is None and y is None:
-            q = torch.empty((T, n), dtype=torch.int8, device=dev)
-            qscale = torch.empty(T, dtype=torch.float32, device=dev)
-        if sum is not None:
-            _need_on(sum, x.dtype, (T, n), dev, "sum")
-        if y is not None:
-            _need_on(y, x.dtype, (T, n), dev, "y")
-        if q is not None:
-            _need_on(q, torch.int8, (T, n), dev, "q")
-            _need_on(qscale, torch.float32, (T,), dev, "qscale")
-        ptr = [None if t is None else t.data_ptr() for t in (residual, sum, y, q, qscale)]
-        _check(LIB.gq_rmsnorm_quantize(x.data_ptr(), ptr[0], xc, gamma.data_ptr(), gc, T, n,
-                                       eps, ptr[1], ptr[2], ptr[3], ptr[4],
-                                       torch.cuda.current_stream(dev).cuda_stream),
-               "gq_rmsnorm_quantize")
+    if residual is not None:
+        _need_on(residual, xt, shape, device, "residual")
+        sum = torch.empty_like(x) if sum is None else sum
+    if q is None and y is None:
+        q = torch.empty(shape, dtype=torch.int8, device=x.device)
+        qscale = torch.empty(T, dtype=torch.float32, device=x.device)
+    if sum is not None:
+        _need_on(sum, xt, shape, device, "sum")
+    if y is not None:
+        _need_on(y, xt, shape, device, "y")
+    if q is not None:
+        _need_on(q, torch.int8, shape, device, "q")
+        _need_on(qscale, torch.float32, (T,), device, "qscale")
+    _check(LIB.gq_rmsnorm_quantize(
+        x.data_ptr(), None if residual is None else residual.data_ptr(), xc, gamma.data_ptr(), gc,
+        T, n, eps, None if sum is None else sum.data_ptr(), None if y is None else y.data_ptr(),
+        None if q is None else q.data_ptr(), None if qscale is None else qscale.data_ptr(),
+        _raw_stream(device)), "gq_rmsnorm_quantize")
     return dict(sum=sum, y=y, q=q, qscale=qscale)
 
 
