@@ -136,27 +136,32 @@ __device__ __forceinline__ const void* token_row(const void* x, int64_t t, int64
   return static_cast<const char*>(x) + t * n * size;
 }
 
+// B words in the widest loads that their size allows (16-byte aligned rows).
+template <int B>
+__device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[B]) {
+  if constexpr (B % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < B / 4; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (B % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < B / 2; ++i) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + i);
+      w[2 * i] = v.x; w[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < B; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  }
+}
+
 // B consecutive words of a row from word w0 on (0 behind the row's end).
 template <int B>
 __device__ __forceinline__ void load_run(const uint32_t* __restrict__ row, int w0, int words,
                                          bool vec, uint32_t (&w)[B]) {
-  if (vec && w0 + B <= words) {
-    if constexpr (B % 4 == 0) {
-#pragma unroll
-      for (int i = 0; i < B / 4; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + w0) + i);
-        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-      }
-      return;
-    } else if constexpr (B % 2 == 0) {
-#pragma unroll
-      for (int i = 0; i < B / 2; ++i) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + w0) + i);
-        w[2 * i] = v.x; w[2 * i + 1] = v.y;
-      }
-      return;
-    }
-  }
+  if (vec && w0 + B <= words) return load_words<B>(reinterpret_cast<const char*>(row + w0), w);
 #pragma unroll
   for (int i = 0; i < B; ++i) w[i] = w0 + i < words ? __ldg(row + w0 + i) : 0u;
 }
@@ -229,8 +234,7 @@ __global__ void __launch_bounds__(kWarps * 32)
           if constexpr (M == kHalves) q.f[r][1] = __ldg(sp[r] + min(g0 + 1, G - 1));
         }
       };
-      auto multiply = [&](int c, const Chunk<B, K, RT>& q) {
-        const bool fast = xvec && c * 128 + 128 <= n;
+      auto multiply = [&](int c, const Chunk<B, K, RT>& q, bool fast) {
         constexpr int kSets = M == kHalves ? 2 : 1;
         uint32_t zz[2 * RT];
 #pragma unroll
@@ -253,7 +257,8 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
           for (int r = 0; r < 2 * RT; ++r) {
             code_pairs<B>(__funnelshift_r(q.w[r][w], q.w[r][w1], sh),
-                          __funnelshift_r(q.w[r][w1], q.w[r][w2], sh), pr[r]);
+                          __funnelshift_r(q.w[r][w1], q.w[r][w2], sh),
+                          pair_other<B, kHalf>(), pr[r]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) pr[r][e] = pair_value<B, kHalf>(pr[r][e], zz[r]);
           }
@@ -293,17 +298,95 @@ __global__ void __launch_bounds__(kWarps * 32)
               for (int i = 0; i < 4; ++i)
                 acc[r][j][i] += q.f[2 * r + (i >> 1)][h] * part[h][r][j][i];
       };
-      Chunk<B, K, RT> q0, q1;
-      int c = warp;
-      if (c < chunks) fetch(c, q0);
-      while (c < chunks) {
-        if (c + kWarps < chunks) fetch(c + kWarps, q1);
-        multiply(c, q0);
-        c += kWarps;
-        if (c >= chunks) break;
-        if (c + kWarps < chunks) fetch(c + kWarps, q0);
-        multiply(c, q1);
-        c += kWarps;
+      // Whole chunks of aligned rows have no bounds to check, and every address is a base of the
+      // block plus a 32-bit offset.  They go to the warps in runs of four: lane t of a quad loads
+      // the scales and zero points of the run's chunk t and hands them round (loaded by every
+      // lane for every chunk they were half of the kernel's L1 wavefronts).
+      const int whole = xvec && cvec ? n / 128 : 0, runs = (whole + 3) / 4;
+      {
+        const char* cb = reinterpret_cast<const char*>(a.codes + row0 * words);
+        const char* sb = reinterpret_cast<const char*>(a.scales + row0 * G);
+        const char* zb = reinterpret_cast<const char*>(a.zeros + row0 * G);
+        constexpr int kPer = M == kHalves ? 2 : 1;  // groups of a chunk
+        uint32_t oc[2 * RT], og[2 * RT];
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) {
+          const int row = (int)min((int64_t)(8 * r + g), a.m - 1 - row0);
+          oc[r] = (uint32_t)(row * words + t * B) * 4;
+          og[r] = (uint32_t)(row * G);
+        }
+        constexpr int kXBytes = K == kXBf16 ? 2 : K == kXFp32 ? 4 : 1;
+        const bool mine = t0 + g < a.T;  // (NT == 1: the other lanes' columns are not stored)
+        const char* xb = static_cast<const char*>(a.x) + t0 * n * kXBytes;
+        const uint32_t ox = (uint32_t)((mine ? g : 0) * n + 32 * t) * kXBytes;
+        struct Run {
+          float f[2 * RT][kPer];
+          uint32_t z[2 * RT][kPer];
+        };
+        auto fetch_run = [&](int b, Run& q) {
+          const uint32_t gi = gshift == 31 ? 0 : (uint32_t)(min(4 * b + t, whole - 1) * kPer);
+#pragma unroll
+          for (int r = 0; r < 2 * RT; ++r)
+#pragma unroll
+            for (int h = 0; h < kPer; ++h) {
+              q.f[r][h] = __ldg(reinterpret_cast<const float*>(sb + (og[r] + gi + h) * 4));
+              q.z[r][h] = __ldg(reinterpret_cast<const uint8_t*>(zb + (og[r] + gi + h)));
+            }
+        };
+        auto fetch_chunk = [&](int c, Chunk<B, K, RT>& q) {
+          if constexpr (NT == 1) {
+            if (mine) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                load_raw<K>(xb + (ox + (uint32_t)c * 128 * kXBytes), 8 * i, n, nullptr, true, q.x[i]);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 2 * RT; ++r) load_words<B>(cb + (oc[r] + (uint32_t)c * 16 * B), q.w[r]);
+        };
+        Chunk<B, K, RT> q[2];
+        if constexpr (NT == 1)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < (int)(sizeof(q[k].x[i].r) / 4); ++e) q[k].x[i].r[e] = 0;
+        Run run, next;
+        if (warp < runs) {
+          fetch_run(warp, next);
+          fetch_chunk(4 * warp, q[0]);
+        }
+        for (int b = warp; b < runs; b += kWarps) {
+          run = next;
+          if (b + kWarps < runs) fetch_run(b + kWarps, next);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int c = 4 * b + k;
+            // the next chunk: of this run, or the first of the warp's next run
+            const int cn = k < 3 && c + 1 < whole ? c + 1 : 4 * (b + kWarps);
+            if (c < whole) {
+              if (cn < whole) fetch_chunk(cn, q[(k + 1) & 1]);
+              const int src = (lane & ~3) | k;
+#pragma unroll
+              for (int r = 0; r < 2 * RT; ++r) {
+#pragma unroll
+                for (int h = 0; h < kPer; ++h) q[k & 1].f[r][h] = __shfl_sync(~0u, run.f[r][h], src);
+                q[k & 1].z[r] = __shfl_sync(~0u, run.z[r][0], src);
+                if constexpr (M == kHalves) {
+                  const uint32_t z1 = __shfl_sync(~0u, run.z[r][1], src);
+                  if (t >= 2) q[k & 1].z[r] = z1;
+                }
+              }
+              multiply(c, q[k & 1], true);
+            }
+          }
+        }
+      }
+      for (int c = whole + warp; c < chunks; c += kWarps) {
+        Chunk<B, K, RT> q;
+        fetch(c, q);
+        multiply(c, q, xvec && c * 128 + 128 <= n);
       }
     } else {
       const bool g16 = gshift == 4;
@@ -332,7 +415,7 @@ __global__ void __launch_bounds__(kWarps * 32)
           float f1[2 * RT];
 #pragma unroll
           for (int r = 0; r < 2 * RT; ++r) {
-            code_pairs<B>(w[r][u][0], w[r][u][1], pr[r]);
+            code_pairs<B>(w[r][u][0], w[r][u][1], pair_other<B, kHalf>(), pr[r]);
             const uint32_t zz = zero_pair<B, kHalf>(z[r][u]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) pr[r][i] = pair_value<B, kHalf>(pr[r][i], zz);
@@ -409,15 +492,17 @@ void launch_mode(const LinearArgs& a, int xvec, cudaStream_t s) {
     const int64_t tiles = (a.T + tokens - 1) / tokens;
     return dim3((unsigned)((a.m + rows - 1) / rows), (unsigned)(tiles < 32768 ? tiles : 32768));
   };
-  // two tiles of rows a warp share the inputs' part of the work; with few rows one tile leaves
-  // more CTAs for the SMs
-  const bool two = a.m >= 2048;
+  // Two tiles of rows a warp share the inputs' part of the work, which is large for fp32 (three
+  // parts) and from a few tokens on; one token of 16 or 8 bits is faster with one tile and more
+  // CTAs (4096 x 4096, 4 bits: one bf16 token 4.5 us against 5.0, eight 6.1 against 5.6, one fp32
+  // token 10.3 against 7.7), as are few rows.
+  const bool two = a.m >= 2048 && (K == kXFp32 || a.T >= 4);
   if (a.T <= 8 && !two)
     linear_rows_kernel<B, K, 1, 1, M, 8><<<grid(16, 8), 256, 0, s>>>(a, gshift, G, xvec, cvec);
   else if (a.T <= 8)
-    linear_rows_kernel<B, K, 1, 2, M, 16><<<grid(32, 8), 512, 0, s>>>(a, gshift, G, xvec, cvec);
+    linear_rows_kernel<B, K, 1, 2, M, 8><<<grid(32, 8), 256, 0, s>>>(a, gshift, G, xvec, cvec);
   else if (a.T <= 16)
-    linear_rows_kernel<B, K, 2, 2, M, 8><<<grid(32, 16), 256, 0, s>>>(a, gshift, G, xvec, cvec);
+    linear_rows_kernel<B, K, 2, 1, M, 8><<<grid(16, 16), 256, 0, s>>>(a, gshift, G, xvec, cvec);
   else
     linear_rows_kernel<B, K, 4, 1, M, 8><<<grid(16, 32), 256, 0, s>>>(a, gshift, G, xvec, cvec);
 }

@@ -457,7 +457,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const uint32_t w0 = w[i][q], w1 = w[i][q + 1 < B ? q + 1 : kTop];
         const uint32_t w2 = w[i][q + 2 < B ? q + 2 : kTop];
         uint32_t pr[4];
-        code_pairs<B>(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh), pr);
+        code_pairs<B>(__funnelshift_r(w0, w1, sh), __funnelshift_r(w1, w2, sh),
+                      pair_other<B, false>(), pr);
         const uint32_t zz = zero_pair<B, false>(z[i][j >> 1]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) pr[e] = pair_value<B, false>(pr[e], zz);

@@ -13,29 +13,40 @@
 
 namespace gq {
 
+// (a & b) | c in one instruction (left to itself the compiler takes two).
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
 // The eight codes of v (bits 0 .. 8B-1; higher bits are ignored) as pairs (i, i + 4) in bits
-// 0..B-1 and 16..16+B-1, the other bits zero.
+// 0..B-1 and 16..16+B-1, the other bits those of `other` (which has none there).
 template <int B>
-__device__ __forceinline__ void code_pairs(uint32_t lo, uint32_t hi, uint32_t (&p)[4]) {
+__device__ __forceinline__ void code_pairs(uint32_t lo, uint32_t hi, uint32_t other,
+                                           uint32_t (&p)[4]) {
   constexpr uint32_t m = ((1u << B) - 1) * 0x00010001u;
   if constexpr (B <= 4) {
     uint32_t t;
     if constexpr (B == 2) t = __byte_perm(lo, 0, 0x4140);
-    if constexpr (B == 3) t = (lo & 0xFFFu) | ((lo << 4) & 0xFFFF0000u);
+    if constexpr (B == 3) t = and_or(lo << 4, 0xFFFF0000u, lo & 0xFFFFu);
     if constexpr (B == 4) t = lo;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = (t >> (i * B)) & m;
+    for (int i = 0; i < 4; ++i) p[i] = and_or(t >> (i * B), m, other);
   } else if constexpr (B == 8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = __byte_perm(lo, hi, 0x0400 + 0x0101 * i) & m;
+    for (int i = 0; i < 4; ++i) p[i] = and_or(__byte_perm(lo, hi, 0x0400 + 0x0101 * i), m, other);
   } else {
-    const uint64_t v = ((uint64_t)hi << 32) | lo;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // codes 2h, 2h + 1 and 2h + 4, 2h + 5
-      const uint32_t a = (uint32_t)(v >> (2 * B * h)), b = (uint32_t)(v >> (4 * B + 2 * B * h));
-      const uint32_t t = (a & 0xFFFFu) | (b << 16);
-      p[2 * h] = t & m;
-      p[2 * h + 1] = ((a >> B) & ((1u << B) - 1)) | (((b >> B) & ((1u << B) - 1)) << 16);
+    for (int h = 0; h < 2; ++h) {
+      // codes 2h, 2h + 1 in the low bits of a, 2h + 4, 2h + 5 in those of b (2B <= 14 bits each)
+      const uint32_t a = h == 0 ? lo : __funnelshift_r(lo, hi, 2 * B);
+      const uint32_t b = h == 0 ? __funnelshift_r(lo, hi, 4 * B)
+                                : 6 * B >= 32 ? hi >> (6 * B >= 32 ? 6 * B - 32 : 0)
+                                              : __funnelshift_r(lo, hi, 6 * B);
+      const uint32_t t = __byte_perm(a, b, 0x5410);
+      p[2 * h] = and_or(t, m, other);
+      p[2 * h + 1] = and_or(t >> B, m, other);
     }
   }
 }
@@ -65,16 +76,22 @@ __device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
   return v * 0x00010001u;
 }
 
-// code - zero of a pair from code_pairs, exact, in bf16 or fp16.
+// What code_pairs puts around the codes for pair_value: the constant of the type.
+template <int B, bool kHalf>
+__device__ __forceinline__ constexpr uint32_t pair_other() {
+  return kHalf ? 0x64006400u : B < 8 ? 0x43004300u : 0u;
+}
+
+// code - zero of a pair from code_pairs with pair_other, exact, in bf16 or fp16.
 template <int B, bool kHalf>
 __device__ __forceinline__ uint32_t pair_value(uint32_t p, uint32_t zp) {
   if constexpr (kHalf) {
-    return f16x2_sub(p | 0x64006400u, zp);
+    return f16x2_sub(p, zp);
   } else if constexpr (B < 8) {
-    return bf16x2_sub(p | 0x43004300u, zp);
+    return bf16x2_sub(p, zp);
   } else {
     // 128 + (c mod 128), then minus 128 where c < 128: every step exact in 8 bits
-    const uint32_t v = (p & 0x007F007Fu) | 0x43004300u;
+    const uint32_t v = and_or(p, 0x007F007Fu, 0x43004300u);
     const uint32_t low = ((~p >> 7) & 0x00010001u) * 0x4300u;
     return bf16x2_sub(bf16x2_sub(v, low), zp);
   }

@@ -12,6 +12,58 @@ import torch
 from . import gq as G
 
 
+class QuantizedLinear:
+    """A quantized layer that runs: y = x W^T from its packed codes (gq_linear, gq_linear_quantized).
+
+    ``codes`` / ``scales`` / ``zeros`` as gq_quantize_layer writes them for a clamped or clip-free
+    layer with uniform spacing.  ``perm`` is the column order of a layer quantized in one: with
+    groups the codes are repacked in that order here, once (without groups they keep their
+    columns).  The tensors are used as they are, not copied, except for that repacking.
+    """
+
+    def __init__(self, codes, scales, zeros, n: int, cfg: G.QuantCfg, perm=None):
+        if cfg.clip == "unbounded" or cfg.spacing != "uniform":
+            raise ValueError("packed codes of uniform spacing only (no unbounded codes, no ZSIC)")
+        if perm is not None and cfg.group_size:
+            codes = G.gq_order_codes(codes, n, cfg.bits, perm)
+        else:
+            perm = None
+        self.codes, self.scales, self.zeros, self.perm = codes, scales, zeros, perm
+        self.n, self.bits, self.group_size = n, cfg.bits, cfg.group_size
+
+    @property
+    def m(self) -> int:
+        return self.codes.shape[0]
+
+    @classmethod
+    def stack(cls, layers):
+        """Layers of one input (same n, bits, groups and order) as one layer, rows one after
+        another: one product for all of them."""
+        layers = list(layers)
+        a = layers[0]
+        for b in layers[1:]:
+            same = (a.n, a.bits, a.group_size) == (b.n, b.bits, b.group_size)
+            if not same or (a.perm is None) != (b.perm is None) or (
+                    a.perm is not None and not torch.equal(a.perm, b.perm)):
+                raise ValueError("stacked layers need the same width, bits, groups and order")
+        one = cls.__new__(cls)
+        one.codes = torch.cat([l.codes for l in layers])
+        one.scales = torch.cat([l.scales for l in layers])
+        one.zeros = torch.cat([l.zeros for l in layers])
+        one.perm, one.n, one.bits, one.group_size = a.perm, a.n, a.bits, a.group_size
+        return one
+
+    def __call__(self, x, qscale=None, y=None, y_dtype=None, ws=None, stream=None):
+        """y (T x m) for tokens x (T x n, bf16 or fp32), or for 8-bit rows x with their scales
+        ``qscale`` (gq_rmsnorm_quantize)."""
+        if qscale is None:
+            return G.gq_linear(x, self.codes, self.scales, self.zeros, self.bits,
+                               self.group_size, self.perm, y, y_dtype, ws, stream)
+        return G.gq_linear_quantized(x, qscale, self.codes, self.scales, self.zeros, self.bits,
+                                     self.group_size, self.perm, y, y_dtype or torch.bfloat16,
+                                     ws, stream)
+
+
 @dataclass
 class LayerResult:
     codes: torch.Tensor    # m x ceil(n b / 32) packed uint32 (int32 view)
@@ -80,6 +132,17 @@ class LayerQuantizer:
         self.prepare(stream=stream)
         self.quantize(W, stream=stream)
         return self.result()
+
+    def linear(self) -> QuantizedLinear:
+        """The quantized layer as one that runs, on this quantizer's own result buffers (the next
+        ``quantize`` writes them; an ordered layer with groups is repacked and keeps its codes)."""
+        return QuantizedLinear(self.codes, self.scales, self.zeros, self.n, self.cfg,
+                               self.perm if self.order else None)
+
+    def output(self, X: torch.Tensor, y=None, stream=None) -> torch.Tensor:
+        """X W^T with the quantized weights, in X's type: the calibration input of what follows
+        this layer, as the quantized model will produce it."""
+        return self.linear()(X, y=y, stream=stream)
 
     def status(self):
         """(prepare status, quantize status, ladder rounds); synchronizes."""
@@ -214,6 +277,30 @@ class BlockQuantizer:
         d, o = self.inputs[key], self.out[name]
         G.gq_quantize_layer(W, d["U"], d["dead"], d["delta"], self.cfg, o["codes"], o["scales"],
                             o["zeros"], o["loss"], self._ws_quant[(m, n)], stream=stream)
+
+    def linear(self, name: str) -> QuantizedLinear:
+        """The quantized layer ``name`` as one that runs, on this quantizer's result buffers."""
+        _, m, n, key = next(l for l in self.layers if l[0] == name)
+        o = self.out[name]
+        return QuantizedLinear(o["codes"], o["scales"], o["zeros"], n, self.cfg)
+
+    def forward(self, key: str, x, gamma, residual=None, eps: float = 1e-6, quantized: bool = True,
+                stream=None) -> dict:
+        """What a decoder runs at the input ``key``: x + residual, its root-mean-square norm with
+        weights gamma, and every quantized layer that reads the input, on the normalised rows in
+        8 bits (``quantized``) or in x's type.  Returns {"sum": x + residual (None without one),
+        layer name: output in x's type}."""
+        names = [l[0] for l in self.layers if l[3] == key]
+        if not names:
+            raise ValueError(f"no layer reads {key!r}")
+        y = None if quantized else torch.empty_like(x)
+        r = G.gq_rmsnorm_quantize(x, gamma, eps, residual=residual, y=y, stream=stream)
+        out = {"sum": r["sum"]}
+        for name in names:
+            f = self.linear(name)
+            out[name] = (f(r["q"], r["qscale"], y_dtype=x.dtype, stream=stream) if quantized
+                         else f(r["y"], stream=stream))
+        return out
 
     def run(self, Ws: dict, Xs: dict, names=None, stream=None) -> dict:
         """The factor of every input that the layers ``names`` (default: all) read, then those

@@ -408,3 +408,71 @@ def test_more_tiles_than_sms(dtype):
     else:
         x = _x(T, n, dtype, 1)
         check_linear(G.gq_linear(x, *dev, bits, group), x.double().cpu().numpy(), w)
+
+
+def test_layer_quantizer_output():
+    """LayerQuantizer.output: the quantized layer on its calibration tokens, natural order and
+    act-order with groups, against the dequantized weights."""
+    from post_weight_quantization_22_b200 import gq as G, synth
+    from post_weight_quantization_22_b200.pipeline import LayerQuantizer
+    from tests.gpu_helpers import unpack_np
+    m, n = 96, 256
+    W, X, _ = synth.workload("q_proj_4096x4096", m=m, n=n, T=300)
+    for order in (None, "act"):
+        cfg = G.QuantCfg(bits=4, group_size=64)
+        lq = LayerQuantizer(m, n, cfg, order=order)
+        lq.run(W.cuda().contiguous(), X.cuda().contiguous())
+        y = lq.output(X.cuda().contiguous())
+        codes = unpack_np(lq.codes.cpu().numpy().view(np.uint32), n, 4)
+        at = np.arange(n) if order is None else np.argsort(lq.perm.cpu().numpy())
+        of = at // 64
+        w = lq.scales.double().cpu().numpy()[:, of] * (codes - lq.zeros.cpu().numpy().astype(int)[:, of])
+        assert y.dtype == torch.bfloat16
+        check_linear(y, X.double().numpy(), w)
+
+
+def test_block_forward_runs_every_layer_of_an_input():
+    """BlockQuantizer.forward: residual, norm, 8-bit rows and q, k, v on them; and the same as one
+    stacked product."""
+    from post_weight_quantization_22_b200 import gq as G, synth
+    from post_weight_quantization_22_b200.pipeline import BlockQuantizer, QuantizedLinear
+    from tests.gpu_helpers import unpack_np
+    layers = (("q", 128, 256, "attn"), ("k", 64, 256, "attn"), ("v", 64, 256, "attn"),
+              ("o", 96, 128, "o"))
+    bq = BlockQuantizer(layers, G.QuantCfg(bits=2, group_size=64))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Ws = {name: (0.02 * torch.randn(m, n, generator=g, device="cuda")).bfloat16()
+          for name, m, n, _ in layers}
+    Xs = {k: torch.randn(400, n, generator=g, device="cuda").bfloat16()
+          for k, n in (("attn", 256), ("o", 128))}
+    bq.run(Ws, Xs)
+    assert bq.status() == 0
+    gamma = (1 + 0.1 * torch.randn(256, generator=g, device="cuda")).bfloat16()
+    for T in (1, 20, 70):
+        x = torch.randn(T, 256, generator=g, device="cuda").bfloat16()
+        res = torch.randn(T, 256, generator=g, device="cuda").bfloat16()
+        out = bq.forward("attn", x, gamma, residual=res)
+        assert set(out) == {"sum", "q", "k", "v"}
+        h, v, q, qs = norm_np(x.double().cpu().numpy(), res.double().cpu().numpy(),
+                              gamma.double().cpu().numpy(), 1e-6, torch.bfloat16)
+        assert np.array_equal(out["sum"].double().cpu().numpy(), h)
+        for name in "qkv":
+            o = bq.out[name]
+            codes = unpack_np(o["codes"].cpu().numpy().view(np.uint32), 256, 2)
+            of = np.arange(256) // 64
+            w = o["scales"].double().cpu().numpy()[:, of] * (
+                codes - o["zeros"].cpu().numpy().astype(int)[:, of])
+            check_linear(out[name], q.astype(np.float64), w, qs.astype(np.float32).astype(np.float64))
+        one = QuantizedLinear.stack([bq.linear(name) for name in "qkv"])
+        r = G.gq_rmsnorm_quantize(x, gamma, 1e-6, residual=res)
+        y = one(r["q"], r["qscale"])
+        assert torch.equal(y, torch.cat([out[name] for name in "qkv"], 1))
+        plain = bq.forward("attn", x, gamma, residual=res, quantized=False)
+        assert torch.equal(plain["sum"], out["sum"]) and plain["q"].dtype == torch.bfloat16
+    with pytest.raises(ValueError):
+        bq.forward("mlp", x, gamma)
+    with pytest.raises(ValueError):
+        QuantizedLinear.stack([bq.linear("q"), bq.linear("o")])
+    with pytest.raises(ValueError):
+        QuantizedLinear(bq.out["q"]["codes"], bq.out["q"]["scales"], bq.out["q"]["zeros"], 256,
+                        G.QuantCfg(bits=2, clip="unbounded"))
