@@ -160,7 +160,8 @@ cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaS
   t.N = pair ? 256 : a.T >= 128 ? 128 : (int)(a.T + 63) / 64 * 64;
   t.mtiles = (int)((a.m + (pair ? 255 : 127)) / (pair ? 256 : 128));
   const int64_t tiles = t.mtiles * ((a.T + t.N - 1) / t.N);
-  t.stages = (int)((a.n + kCols - 1) / kCols);
+  // (a pair's in whole packed chunks: what lies behind the last column reads as zero)
+  t.stages = pair ? (int)((a.n + 127) / 128 * 2) : (int)((a.n + kCols - 1) / kCols);
   t.hdr = static_cast<WsHeader*>(ws);
   t.gshift = a.group ? __builtin_ctz((unsigned)a.group) : 31;
   t.dmask = a.group ? a.group / 16 - 1 : 15;

@@ -49,11 +49,10 @@ constexpr int lin_chunks(int B, int P) {
 }
 
 
-// Waits as mbar_wait (acquire at cluster scope), but also gives up when another role of the CTA
-// has.
+// Waits as mbar_wait, but also gives up when another role of the CTA has.
 __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, volatile int* fail) {
   for (uint32_t i = 0; i < tc::kDefaultPolls; ++i) {
-    if (tc::mbar_try_wait_cluster(bar, parity)) return true;
+    if (tc::mbar_try_wait(bar, parity)) return true;
     if ((i & 1023) == 1023 && *fail) return false;
   }
   *fail = 1;
@@ -373,7 +372,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               if (first && period >= 2 && !free_seen)
                 ok = wait_or_fail(&t_empty[period & 1], ((period >> 1) - 1) & 1, fail);
               if (!ok) break;
-              seen = tc::mbar_test_wait_cluster(&full[s_next], ph_next);
+              seen = tc::mbar_test_wait(&full[s_next], ph_next);
               tc::fence_after_sync();
               const uint32_t d = tmem + (period & 1) * kN;
 #pragma unroll
@@ -386,10 +385,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 commit(&t_full[period & 1]);
                 ++period;
                 free_seen = period >= 2 &&
-                            tc::mbar_test_wait_cluster(&t_empty[period & 1], ((period >> 1) - 1) & 1);
+                            tc::mbar_test_wait(&t_empty[period & 1], ((period >> 1) - 1) & 1);
               }
             } else {  // groups of 16 or 32 columns: several periods in a stage
-              seen = tc::mbar_test_wait_cluster(&full[s_next], ph_next);
+              seen = tc::mbar_test_wait(&full[s_next], ph_next);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const bool first = (step & dmask) == 0;
@@ -471,9 +470,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         *reinterpret_cast<uint4*>(tilep + r * 128 + ((blk ^ (r & 7)) << 4)) = v;
       }
     };
-    // the stages of all tiles in one count: this role's are odd, odd + 2, ..
+    // The stages of all tiles in one count: this role's are odd, odd + 2, ..  (A pair's tile has an
+    // even number of them, so that both roles read every packed chunk: a role that left one out
+    // could take the phase before a chunk's barrier for the phase it waits for.)
     int tile = tile0, st = odd, chunk0 = 0;  // chunk0: packed chunks of the tiles before
-    const int per_tile = (ns + 1) / 2;
+    const int per_tile = ns / 2;
     while (st >= ns && tile < a.tiles) {
       st -= ns;
       tile += tstep;
@@ -498,7 +499,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
       if (use > 0 && !warp_wait(&empty[s], (use - 1) & 1, fail)) break;
       uint8_t* tilep = base + s * kStage;
-      const bool alone = st + 1 == ns && !(st & 1);  // the chunk's other half is behind the end
       int next = tile;
       st += 2;
       while (st >= ns && next < a.tiles) {
@@ -520,10 +520,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       tc::fence_proxy_async_smem();
       arrive(full_at + 8 * s);
       if constexpr (kPair) {
-        if (lane == 0) {
-          tc::mbar_arrive(&c_empty[cs]);
-          if (alone) tc::mbar_arrive(&c_empty[cs]);
-        }
+        if (lane == 0) tc::mbar_arrive(&c_empty[cs]);
       }
       s += 2;
       if (s >= kStages) {

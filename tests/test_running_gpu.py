@@ -476,3 +476,25 @@ def test_block_forward_runs_every_layer_of_an_input():
     with pytest.raises(ValueError):
         QuantizedLinear(bq.out["q"]["codes"], bq.out["q"]["scales"], bq.out["q"]["zeros"], 256,
                         G.QuantCfg(bits=2, clip="unbounded"))
+
+
+@pytest.mark.parametrize("bits", (2, 4, 6, 8))
+@pytest.mark.parametrize("dtype", (torch.bfloat16, torch.float32))
+def test_half_a_chunk_at_the_end_of_many_tiles(bits, dtype):
+    """Widths that end inside a packed chunk of 128 columns (an odd number of 64-column stages),
+    with several tiles for every pair of SMs."""
+    from post_weight_quantization_22_b200 import gq as G
+    for m, n, T, group in ((2560, 192, 4000, 64), (2560, 64, 4000, 0), (2600, 448, 2100, 32)):
+        c, s, z, w = layer_np(m, n, bits, group, n + bits)
+        dev = to_cuda(c, s, z, bits)
+        x = _x(T, n, dtype, 1)
+        first = G.gq_linear(x, *dev, bits, group, y_dtype=torch.float32)
+        rows = np.r_[0:40, T - 40:T]
+        check_linear(first[rows], x.double().cpu().numpy()[rows], w)
+        ref = x.double() @ torch.from_numpy(w).cuda().T
+        A = x.double().abs() @ torch.from_numpy(np.abs(w)).cuda().T
+        # the bound of check_linear (fp32 output) for the rest
+        sums = 3 * 256 * 2.0 ** -23 + (n / 16 + 18) * 2.0 ** -24
+        assert bool(((first.double() - ref).abs() <= 2.0 ** -24 * ref.abs() + 1.01 * sums * A).all())
+        for _ in range(5):
+            assert torch.equal(G.gq_linear(x, *dev, bits, group, y_dtype=torch.float32), first)
