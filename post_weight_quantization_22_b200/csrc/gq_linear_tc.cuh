@@ -31,11 +31,14 @@ namespace {
 constexpr int kLinThreads = 640;
 constexpr int kUnpackWarp = 4, kScaleWarp = 12;   // first warps of these roles, 8 each
 // Registers a thread of the three roles holds, in warpgroups of 128 threads: together what the
-// launch has (96 x 640).  A scaling thread holds 128 sums.
-#define GQ_LIN_REGS_CONTROL "32"
-#define GQ_LIN_REGS_UNPACK "48"
-#define GQ_LIN_REGS_SCALE "176"
-#define GQ_LIN_REGS_LAUNCH "96"
+// launch has (96 x 640).  A pair's scaling thread holds 128 sums, a single CTA's 64.
+constexpr int kRegsLaunch = 96;
+template <bool kPair>
+struct LinRegs {
+  static constexpr int control = kPair ? 32 : 64, unpack = kPair ? 48 : 88,
+                       scale = kPair ? 176 : 120;
+  static_assert(control + 2 * unpack + 2 * scale == 5 * kRegsLaunch, "register shares");
+};
 constexpr uint32_t kTile = 128 * kCols * 2;       // 128 rows or tokens of them, 128 bytes each
 constexpr uint32_t kOutStage = 1024;              // a scaling warp's output staging
 // Shared memory: the ring of stages (each the unpacked rows and P parts of the tokens), the
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   };
 
   if (warp < kUnpackWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 " GQ_LIN_REGS_CONTROL ";");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LinRegs<kPair>::control));
     if (warp == 0) {
       if (tc::elect_one()) {
         // tokens: 64 columns of every part per stage
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     __syncwarp();
   } else if (warp < kScaleWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 " GQ_LIN_REGS_UNPACK ";");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LinRegs<kPair>::unpack));
     // Unpack.  Warps 4-7 fill the even stages, 8-11 the odd ones; a thread takes one unit of 32
     // columns in each of two rows (a warp reads 16 rows x 8 b bytes at a time; its 16-byte stores
     // of one column block fall on 8 different rows in every quarter, so the swizzled tile takes
@@ -510,15 +513,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       if (more && next != tile) rows_of(next);
       tile = next;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        store_unit(tilep, i);
-        if (more) {  // in flight until this role's next stage
+      for (int i = 0; i < 2; ++i) store_unit(tilep, i);
+      tc::fence_proxy_async_smem();
+      arrive(full_at + 8 * s);
+      // the next stage's loads only now: the fence waits for every access in flight
+      if (more) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
           load_zeros(st, i);
           load_words(st, i);
         }
       }
-      tc::fence_proxy_async_smem();
-      arrive(full_at + 8 * s);
       if constexpr (kPair) {
         if (lane == 0) tc::mbar_arrive(&c_empty[cs]);
       }
@@ -529,7 +534,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 " GQ_LIN_REGS_SCALE ";");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LinRegs<kPair>::scale));
     // scale and add: thread = row, this warp's half of the tokens
     const int half = (warp - kScaleWarp) >> 2, quarter = warp & 3;
     const int G = a.groups;
@@ -605,9 +610,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // smaller shares may not grow before the larger one has been taken and given back, or it could
   // never be taken.
   if (warp >= kScaleWarp)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 " GQ_LIN_REGS_LAUNCH ";");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
   else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 " GQ_LIN_REGS_LAUNCH ";");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
   if (warp == 1 && lane == 0) tc::mbar_wait(done, 0);  // also after a failure: no MMA in flight
   __syncwarp();
   if constexpr (kPair) {

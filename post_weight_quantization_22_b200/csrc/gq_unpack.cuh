@@ -29,7 +29,7 @@ __device__ __forceinline__ void code_pairs(uint32_t lo, uint32_t hi, uint32_t ot
   if constexpr (B <= 4) {
     uint32_t t;
     if constexpr (B == 2) t = __byte_perm(lo, 0, 0x4140);
-    if constexpr (B == 3) t = and_or(lo << 4, 0xFFFF0000u, lo & 0xFFFFu);
+    if constexpr (B == 3) t = __byte_perm(lo, lo << 4, 0x7610);
     if constexpr (B == 4) t = lo;
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = and_or(t >> (i * B), m, other);
