@@ -128,7 +128,8 @@ cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaS
   // a misaligned matrix cannot be a tensor map: the warp-level kernel reads it in place
   const bool aligned = p.staged || reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
   const int64_t rows_total = (int64_t)p.P * a.T;
-  if (!p.tc || !aligned || rows_total > INT32_MAX) return launch_linear_rows(a, kind, s);
+  // (tile coordinates are 32-bit)
+  if (!p.tc || !aligned || rows_total > INT32_MAX - 1024) return launch_linear_rows(a, kind, s);
   const void* xt = a.x;
   int64_t ld = a.n, cols = a.n;
   if (p.staged) {

@@ -82,28 +82,38 @@ __device__ __forceinline__ void store8(T* row, int64_t i0, int64_t step, int64_t
   }
 }
 
-// Sum and maximum over the block (blockDim.x a multiple of 32).
-__device__ __forceinline__ void block_reduce(double& ss, unsigned long long& top, double* rs,
-                                             unsigned long long* rt) {
+// Sum and maximum over the block (blockDim.x a multiple of 32), the same in every thread.  Two
+// scratch halves taken in turn: one barrier a call.
+struct NormScratch {
+  double s[2][kNMaxThreads / 32];
+  unsigned long long t[2][kNMaxThreads / 32];
+};
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    ss += __shfl_xor_sync(~0u, ss, o);
-    top = max(top, __shfl_xor_sync(~0u, top, o));
-  }
-  const int warps = blockDim.x >> 5;
+  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(~0u, v, o));
+  return v;
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(~0u, v); }
+template <class U>
+__device__ __forceinline__ void block_reduce(double& ss, U& top, NormScratch& m, int& half) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+  top = warp_max(top);
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
   if (warps == 1) return;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
-    rs[threadIdx.x >> 5] = ss;
-    rt[threadIdx.x >> 5] = top;
+  if (lane == 0) {
+    m.s[half][threadIdx.x >> 5] = ss;
+    m.t[half][threadIdx.x >> 5] = top;
   }
   __syncthreads();
-  ss = 0.0;
-  top = 0;
-  for (int w = 0; w < warps; ++w) {
-    ss += rs[w];
-    top = max(top, rt[w]);
-  }
+  ss = lane < warps ? m.s[half][lane] : 0.0;
+  top = lane < warps ? (U)m.t[half][lane] : 0;
+  static_assert(kNMaxThreads / 32 <= 16, "the sums of the warps lie in sixteen lanes");
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+  ss = __shfl_sync(~0u, ss, 0);
+  top = warp_max(top);
+  half ^= 1;
 }
 __device__ __forceinline__ unsigned long long abs_bits(double v) {
   return (unsigned long long)__double_as_longlong(v) & 0x7FFFFFFFFFFFFFFFull;
@@ -126,8 +136,8 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 256, V <= 2 ? 3 : V == 4 ? 2 : 
   constexpr bool kExact32 = sizeof(X) == 2 && sizeof(Gm) == 2;  // u is exact in fp32
   constexpr bool kKeep = kExact32 && V <= 2;  // gamma and u stay in registers
   constexpr float kMagic = 12582912.f;        // 1.5 * 2^23
-  __shared__ double rs[kNMaxThreads / 32];
-  __shared__ unsigned long long rt[kNMaxThreads / 32];
+  __shared__ NormScratch scratch;
+  int half = 0;
   const int64_t n = a.n;
   const int nt = blockDim.x, tid = threadIdx.x;
   const int64_t step = kVec ? 1 : nt;
@@ -192,8 +202,13 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 256, V <= 2 ? 3 : V == 4 ? 2 : 
         }
       }
     }
-    if constexpr (kExact32) top = abs_bits((double)top32);
-    block_reduce(ss, top, rs, rt);
+    if constexpr (kExact32) {
+      uint32_t bits = __float_as_uint(top32);
+      block_reduce(ss, bits, scratch, half);
+      top = abs_bits((double)__uint_as_float(bits));
+    } else {
+      block_reduce(ss, top, scratch, half);
+    }
     double topd = __longlong_as_double((long long)top);
     if constexpr (kExact32) {
       // fp32 products that left the normal range: the row's maximum again, in fp64
@@ -212,7 +227,7 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 256, V <= 2 ? 3 : V == 4 ? 2 : 
           for (int e = 0; e < 8; ++e)
             top = max(top, abs_bits((double)to_f32(hk.v[e]) * (double)to_f32(g.v[e])));
         }
-        block_reduce(none, top, rs, rt);
+        block_reduce(none, top, scratch, half);
         topd = __longlong_as_double((long long)top);
       }
     }
@@ -288,10 +303,12 @@ void launch_v(const NormArgs& a, int nt, cudaStream_t s) {
 }
 template <class X, class Gm, bool kVec>
 void launch_row(const NormArgs& a, cudaStream_t s) {
-  // a thread for each vector of eight up to 256 threads, then more vectors a thread
+  // A thread for each vector of eight up to 256 threads, then more vectors a thread; with rows
+  // enough two vectors a thread from the start (8192 x 1024 bf16: 13 us against 17).
   const int64_t nv = (a.n + 7) / 8;
+  const int per = a.T >= 8 * kNSMs ? 2 : 1;
   int nt = 32;
-  while (nt < 256 && nt < nv) nt *= 2;
+  while (nt < 256 && nt * per < nv) nt *= 2;
   if (nv > 8 * nt) nt = kNMaxThreads;
   if (nv <= nt) launch_v<X, Gm, 1, kVec>(a, nt, s);
   else if (nv <= 2 * nt) launch_v<X, Gm, 2, kVec>(a, nt, s);
