@@ -382,9 +382,9 @@ gq_status gq_huffman_encode(const int32_t* d_codes, int64_t count, uint64_t* d_s
  * papers have no counterpart of them.  They cover the packed formats: uniform spacing, clip 0
  * or 1, any order.  (The unconstrained integers of clip = 2, ZSIC's per-column steps and SSQR's
  * outliers are not part of the packed stream.)  A workspace serves one call at a time: calls
- * whose work may overlap need one each.  After gq_linear or gq_linear_quantized with more than 32
- * tokens its status word (gq_workspace_status) holds GQ_OK, or GQ_ERR_TIMEOUT if a bounded device
- * wait ran out (d_y is then undefined).
+ * whose work may overlap need one each.  After a call that needed a workspace its status word
+ * (gq_workspace_status) holds GQ_OK, or GQ_ERR_TIMEOUT if a bounded device wait ran out (d_y is
+ * then undefined).
  */
 
 /*

@@ -41,8 +41,20 @@ gq_status ensure_device_setup() {
   if (lazy_tc_init_attributes() != cudaSuccess) return GQ_ERR_CUDA;
   if (hessian_init_attributes() != cudaSuccess) return GQ_ERR_CUDA;
   if (huffman_init_attributes() != cudaSuccess) return GQ_ERR_CUDA;
-  if (linear_init_attributes() != cudaSuccess) return GQ_ERR_CUDA;
   g_init_done[dev] = true;
+  return GQ_OK;
+}
+
+// The packed products' kernels (one set per code width) are set up by their own first call, so
+// that the other calls do not load them.
+bool g_linear_done[128] = {};
+gq_status ensure_linear_setup() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return GQ_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_init_mu);
+  if (g_linear_done[dev]) return GQ_OK;
+  if (linear_init_attributes() != cudaSuccess) return GQ_ERR_CUDA;
+  g_linear_done[dev] = true;
   return GQ_OK;
 }
 
@@ -385,7 +397,7 @@ static size_t linear_ws(int64_t T, int64_t m, int64_t n, int kind, int ordered) 
   if (T < 0 || T > kMaxT || m < 1 || m > kMaxM || n < 1 || n > kMaxN) return 0;
   if (ordered != 0 && ordered != 1) return 0;
   if (kind != kXBf16 && kind != kXFp32 && kind != kXInt8) return 0;
-  return linear_ws_bytes(T, n, (LinearInput)kind, ordered != 0);
+  return linear_ws_bytes(T, m, n, (LinearInput)kind, ordered != 0);
 }
 
 size_t gq_linear_workspace_size(int64_t T, int64_t m, int64_t n, gq_dtype x_dtype, int ordered) {
@@ -415,7 +427,8 @@ static gq_status linear_common(const LinearArgs& a, LinearInput kind, gq_dtype y
     return GQ_ERR_INVALID_ARG;
   const size_t need = linear_ws(a.T, a.m, a.n, kind, a.perm != nullptr);
   if (need > 0 && (!d_ws || !aligned256(d_ws) || ws_bytes < need)) return GQ_ERR_WORKSPACE;
-  gq_status st = ensure_device_setup();
+  // (only the tcgen05 kernels, the calls with a workspace, need any)
+  const gq_status st = need > 0 ? ensure_linear_setup() : GQ_OK;
   if (st != GQ_OK) return st;
   return launch_linear(a, kind, d_ws, (cudaStream_t)stream) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
 }

@@ -231,7 +231,7 @@ struct LinearArgs {
 // The product on the warp-level tensor cores, for few tokens (correct for any T).
 cudaError_t launch_linear_rows(const LinearArgs& a, LinearInput kind, cudaStream_t s);
 // The product by the kernel that fits its sizes (gq_linear_tc.cu); ws of linear_ws_bytes.
-size_t linear_ws_bytes(int64_t T, int64_t n, LinearInput kind, bool ordered);
+size_t linear_ws_bytes(int64_t T, int64_t m, int64_t n, LinearInput kind, bool ordered);
 cudaError_t linear_init_attributes();
 cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaStream_t s);
 cudaError_t launch_order_codes(const uint32_t* codes, int64_t m, int64_t n, int bits,

@@ -9,26 +9,64 @@
 namespace gq {
 
 // ---- tokens as bf16 parts: P x T rows of ld elements, columns behind n zero ----
+// One block a row, eight columns a thread (16-byte stores; 16-byte loads where vec says that rows
+// are aligned and taken in order).
 template <LinearInput K>
-__global__ void linear_stage_kernel(const void* __restrict__ x, int64_t T, int64_t n, int64_t ld,
-                                    const int32_t* __restrict__ perm, uint16_t* __restrict__ out) {
+__global__ void linear_stage_kernel(const void* __restrict__ x, int64_t T, int n, int ld,
+                                    const int32_t* __restrict__ perm, int vec,
+                                    uint16_t* __restrict__ out) {
+  constexpr int kSize = K == kXBf16 ? 2 : K == kXFp32 ? 4 : 1;
+  constexpr int P = K == kXFp32 ? 3 : 1;
   const int64_t t = blockIdx.x;
-  for (int64_t k = threadIdx.x; k < ld; k += blockDim.x) {
-    const int64_t src = t * n + (k < n ? (perm ? perm_at(perm, k, n) : k) : 0);
-    uint16_t* o = out + t * ld + k;
-    if constexpr (K == kXFp32) {
-      const float v = k < n ? static_cast<const float*>(x)[src] : 0.f;
-      uint32_t h, m, l;
-      split3(v, h, m, l);
-      o[0] = (uint16_t)(h >> 16);
-      o[T * ld] = (uint16_t)(m >> 16);
-      o[2 * T * ld] = (uint16_t)(l >> 16);
-    } else if constexpr (K == kXInt8) {
-      const float v = k < n ? (float)static_cast<const int8_t*>(x)[src] : 0.f;
-      o[0] = __bfloat16_as_ushort(__float2bfloat16(v));
+  const char* row = static_cast<const char*>(x) + t * n * kSize;
+  for (int k = threadIdx.x * 8; k < ld; k += blockDim.x * 8) {
+    alignas(16) char in[8 * kSize];
+    if (vec && k + 8 <= n) {
+      if constexpr (K == kXInt8) {
+        *reinterpret_cast<uint2*>(in) = __ldg(reinterpret_cast<const uint2*>(row + k));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kSize / 2; ++i)
+          reinterpret_cast<uint4*>(in)[i] =
+              __ldg(reinterpret_cast<const uint4*>(row + (int64_t)k * kSize) + i);
+      }
     } else {
-      o[0] = k < n ? static_cast<const uint16_t*>(x)[src] : (uint16_t)0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t src = k + i < n ? (perm ? perm_at(perm, k + i, n) : k + i) : -1;
+        if constexpr (K == kXInt8)
+          in[i] = src < 0 ? 0 : __ldg(reinterpret_cast<const signed char*>(row) + src);
+        else if constexpr (K == kXBf16)
+          reinterpret_cast<uint16_t*>(in)[i] =
+              src < 0 ? (uint16_t)0 : __ldg(reinterpret_cast<const uint16_t*>(row) + src);
+        else
+          reinterpret_cast<float*>(in)[i] =
+              src < 0 ? 0.f : __ldg(reinterpret_cast<const float*>(row) + src);
+      }
     }
+    uint32_t part[P][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (K == kXFp32) {
+        const float* f = reinterpret_cast<const float*>(in) + 2 * i;
+        uint32_t h0, m0, l0, h1, m1, l1;
+        split3(f[0], h0, m0, l0);
+        split3(f[1], h1, m1, l1);
+        part[0][i] = __byte_perm(h0, h1, 0x7632);
+        part[1][i] = __byte_perm(m0, m1, 0x7632);
+        part[2][i] = __byte_perm(l0, l1, 0x7632);
+      } else if constexpr (K == kXInt8) {
+        const signed char* c = reinterpret_cast<const signed char*>(in) + 2 * i;
+        const __nv_bfloat162 v = __floats2bfloat162_rn((float)c[0], (float)c[1]);  // exact
+        part[0][i] = reinterpret_cast<const uint32_t&>(v);
+      } else {
+        part[0][i] = reinterpret_cast<const uint32_t*>(in)[i];
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      *reinterpret_cast<uint4*>(out + (p * T + t) * ld + k) =
+          make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
   }
 }
 
@@ -39,9 +77,13 @@ struct LinPlan {
   int P;
   int64_t ld;      // staged row length, elements
 };
-LinPlan plan_of(int64_t T, int64_t n, LinearInput kind, bool ordered) {
+LinPlan plan_of(int64_t T, int64_t m, int64_t n, LinearInput kind, bool ordered) {
   LinPlan p{};
-  p.tc = T > 32;
+  // The warp-level kernel up to 32 tokens, and further while its CTAs (16 rows x 32 tokens) fit
+  // the SMs once, where the tcgen05 kernel's fixed steps weigh more (48 tokens, 1024 x 4096, 2
+  // bits: 9.0 us against 12.6; 64 tokens, 4096 x 4096: 32 against 18); not for fp32, whose parts
+  // cost it three products (23 us against 16).
+  p.tc = T > 32 && (kind == kXFp32 || (m + 15) / 16 * ((T + 31) / 32) > kSMs);
   p.P = kind == kXFp32 ? 3 : 1;
   // TMA takes rows whose length is a multiple of 16 bytes
   p.staged = kind != kXBf16 || ordered || n % 8 != 0;
@@ -95,18 +137,27 @@ cudaError_t launch_order_codes(const uint32_t* codes, int64_t m, int64_t n, int 
   return cudaGetLastError();
 }
 
-size_t linear_ws_bytes(int64_t T, int64_t n, LinearInput kind, bool ordered) {
-  const LinPlan p = plan_of(T, n, kind, ordered);
+size_t linear_ws_bytes(int64_t T, int64_t m, int64_t n, LinearInput kind, bool ordered) {
+  const LinPlan p = plan_of(T, m, n, kind, ordered);
   if (!p.tc) return 0;
   return kAlign + (p.staged ? align_up((size_t)p.P * T * p.ld * 2) : 0);
 }
+
+namespace {
+// clusters of 2^i CTAs that a device runs at once (written once per device, before its first call)
+int g_clusters[128][4];
+}  // namespace
 
 cudaError_t linear_init_attributes() {
   for (int b = 2; b <= 8; ++b) {
     const cudaError_t e = at_bits(b, [](auto w) { return linear_tc_init<decltype(w)::value>(); });
     if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  for (int i = 1; i <= 3 && e == cudaSuccess; ++i)
+    e = linear_tc_clusters<4>(1 << i, &g_clusters[dev & 127][i]);
+  return e;
 }
 
 cudaError_t launch_linear_rows(const LinearArgs& a, LinearInput kind, cudaStream_t s) {
@@ -124,7 +175,7 @@ cudaError_t launch_linear_rows(const LinearArgs& a, LinearInput kind, cudaStream
 
 cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  const LinPlan p = plan_of(a.T, a.n, kind, a.perm != nullptr);
+  const LinPlan p = plan_of(a.T, a.m, a.n, kind, a.perm != nullptr);
   // a misaligned matrix cannot be a tensor map: the warp-level kernel reads it in place
   const bool aligned = p.staged || reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
   const int64_t rows_total = (int64_t)p.P * a.T;
@@ -135,12 +186,17 @@ cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaS
   if (p.staged) {
     uint16_t* out = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kAlign);
     const unsigned grid = (unsigned)a.T;
+    const int row_bytes = (int)a.n * (kind == kXFp32 ? 4 : kind == kXInt8 ? 1 : 2);
+    const int align = kind == kXInt8 ? 8 : 16;
+    const int xvec = !a.perm && row_bytes % align == 0 &&
+                     reinterpret_cast<uintptr_t>(a.x) % align == 0;
+    const int nt = p.ld >= 2048 ? 256 : 64;
     if (kind == kXFp32)
-      linear_stage_kernel<kXFp32><<<grid, 256, 0, s>>>(a.x, a.T, a.n, p.ld, a.perm, out);
+      linear_stage_kernel<kXFp32><<<grid, nt, 0, s>>>(a.x, a.T, (int)a.n, (int)p.ld, a.perm, xvec, out);
     else if (kind == kXInt8)
-      linear_stage_kernel<kXInt8><<<grid, 256, 0, s>>>(a.x, a.T, a.n, p.ld, a.perm, out);
+      linear_stage_kernel<kXInt8><<<grid, nt, 0, s>>>(a.x, a.T, (int)a.n, (int)p.ld, a.perm, xvec, out);
     else
-      linear_stage_kernel<kXBf16><<<grid, 256, 0, s>>>(a.x, a.T, a.n, p.ld, a.perm, out);
+      linear_stage_kernel<kXBf16><<<grid, nt, 0, s>>>(a.x, a.T, (int)a.n, (int)p.ld, a.perm, xvec, out);
     count_launches(1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -169,9 +225,13 @@ cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaS
   t.groups = a.group ? (int)((a.n + a.group - 1) / a.group) : 1;
   if (tiles > INT32_MAX - kSMs) return cudaErrorInvalidValue;
   t.tiles = (int)tiles;
-  // columns shared by a cluster while tiles leave SMs idle and every CTA keeps eight stages
-  int S = 1;
-  while (!pair && S < 8 && tiles * S * 2 <= kSMs && t.stages >= S * 16) S *= 2;
+  // Columns shared by a cluster while the device runs all clusters at once and every CTA keeps
+  // eight stages.  (Clusters of eight do not fill every group of SMs: sixteen of them took two
+  // waves, 24 us where clusters of four take 17.)
+  int dev = 0, S = 1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  for (int i = 1; !pair && i <= 3; ++i)
+    if (tiles <= g_clusters[dev & 127][i] && t.stages >= 8 << i) S = 1 << i;
   CUtensorMap map;
   cudaError_t e = encode_tmap_2d(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, xt, rows_total, cols,
                                  ld, kCols, (uint32_t)(pair ? 128 : t.N), CU_TENSOR_MAP_SWIZZLE_128B);

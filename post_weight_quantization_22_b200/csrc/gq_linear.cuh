@@ -31,5 +31,8 @@ cudaError_t linear_tc_bits(const CUtensorMap& map, const LinTcArgs& a, int P, bo
                            int wide, int S, cudaStream_t s);
 template <int B>
 cudaError_t linear_tc_init();
+// How many clusters of S CTAs of the single form the current device runs at once.
+template <int B>
+cudaError_t linear_tc_clusters(int S, int* count);
 
 }  // namespace gq

@@ -12,4 +12,5 @@ template void linear_rows_bits<GQ_LINEAR_BITS>(const LinearArgs&, LinearInput, i
 template cudaError_t linear_tc_bits<GQ_LINEAR_BITS>(const CUtensorMap&, const LinTcArgs&, int, bool,
                                                     int, int, int, cudaStream_t);
 template cudaError_t linear_tc_init<GQ_LINEAR_BITS>();
+template cudaError_t linear_tc_clusters<GQ_LINEAR_BITS>(int, int*);
 }  // namespace gq

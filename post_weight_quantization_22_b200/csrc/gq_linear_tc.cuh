@@ -698,6 +698,21 @@ cudaError_t init_one() {
 }  // namespace
 
 template <int B>
+cudaError_t linear_tc_clusters(int S, int* count) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)S);
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = kLinSmem;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)S;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(count, linear_tc_kernel<B, 1, false>, &cfg);
+}
+
+template <int B>
 cudaError_t linear_tc_init() {
   cudaError_t e;
   if ((e = init_one<B, 3, false>())) return e;

@@ -94,15 +94,17 @@ def test_workspace_queries():
 
 def test_many_tokens_need_their_workspace():
     from post_weight_quantization_22_b200 import gq as G
-    need = G.gq_linear_workspace_size(64, 8, 16, torch.float32)
+    m = 4096
+    need = G.gq_linear_workspace_size(64, m, 16, torch.float32)
     assert need >= 3 * 64 * 16 * 2                      # three bf16 parts of the tokens
-    assert G.gq_linear_workspace_size(64, 8, 16, torch.bfloat16) == 256
-    assert G.gq_linear_workspace_size(64, 8, 16, torch.bfloat16, ordered=True) > 256
-    assert G.gq_linear_workspace_size(64, 8, 17, torch.bfloat16) > 256
-    assert _linear(T=64, ws=None, nws=0) == WORKSPACE
-    assert _linear(T=64, xt=1, nws=need - 1) == WORKSPACE
-    assert _linear(T=64, ws=ctypes.c_void_p(4096 + 128)) == WORKSPACE
-    assert _quantized(T=64, ws=None, nws=0) == WORKSPACE
+    assert G.gq_linear_workspace_size(64, m, 16, torch.bfloat16) == 256
+    assert G.gq_linear_workspace_size(64, m, 16, torch.bfloat16, ordered=True) > 256
+    assert G.gq_linear_workspace_size(64, m, 17, torch.bfloat16) > 256
+    assert G.gq_linear_workspace_size(48, 256, 16, torch.bfloat16) == 0  # few rows: none
+    assert _linear(T=64, m=m, ws=None, nws=0) == WORKSPACE
+    assert _linear(T=64, m=m, xt=1, nws=need - 1) == WORKSPACE
+    assert _linear(T=64, m=m, ws=ctypes.c_void_p(4096 + 128)) == WORKSPACE
+    assert _quantized(T=64, m=m, ws=None, nws=0) == WORKSPACE
 
 
 def test_binding_refuses_cpu_tensors_and_wrong_shapes():
