@@ -9,7 +9,7 @@
 // lane t of a quad takes columns 32 t .. 32 t + 31 of its two rows: b whole words of the stream, in
 // 16-byte loads where rows are aligned.  With groups of 64 two lanes of a quad hold one group and
 // two the other; the chunk is then multiplied twice, with the other half's inputs at zero.
-// Groups of 32 and 16 take units of 32 columns instead, 8 columns a lane.
+// Groups of 32 and 16 are multiplied one by one in the same way.
 // c - z is an exact integer in 16 bits, the products are exact, and the fp32 sums of one group
 // are multiplied by the group's scale in fp32: no weight is rounded.  The warps of a CTA share
 // the columns in chunks of 128 and add their sums in a fixed order; every warp loads a chunk
@@ -37,30 +37,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The lane's eight codes of one unit: bits [8 t B, 8 (t + 1) B) of the unit's B words.
-template <int B>
-__device__ __forceinline__ void load_codes(const uint32_t* __restrict__ row, int unit, int t,
-                                           int words, uint32_t& lo, uint32_t& hi) {
-  const int w = unit * B + (t * B) / 4;
-  const uint32_t shift = 8 * ((t * B) % 4);
-  const uint32_t w0 = w < words ? __ldg(row + w) : 0u;
-  if constexpr (B == 4) {
-    lo = w0;
-    hi = 0;
-  } else if constexpr (B == 2) {
-    lo = w0 >> shift;
-    hi = 0;
-  } else {
-    const uint32_t w1 = w + 1 < words ? __ldg(row + w + 1) : 0u;
-    lo = __funnelshift_r(w0, w1, shift);
-    hi = w1 >> shift;
-    if constexpr (B == 7) {
-      const uint32_t w2 = w + 2 < words ? __ldg(row + w + 2) : 0u;
-      hi = __funnelshift_r(w1, w2, shift);
-    }
-  }
 }
 
 // Eight inputs x[k .. k+7] of one token as they lie in memory.
@@ -174,9 +150,8 @@ struct Chunk {
   float f[2 * RT][2];     // scales of the chunk's group, or of its halves'
   Raw<K> x[4];
 };
-// How a chunk's columns fall into groups: one group or more of 128 columns, halves of 64, or units
-// of 32 and 16.
-enum GroupMode { kWhole = 0, kHalves = 1, kFine = 2 };
+// The groups in a chunk of 128 columns (a row's one grid counts as one).
+enum GroupMode { kWhole = 1, kHalves = 2, kQuarters = 4, kEighths = 8 };
 }  // namespace
 
 // One CTA: 16 RT rows x (8 NT) tokens.  gshift: log2 of the group width (31: one grid per row).
@@ -216,7 +191,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
     for (int j = 0; j < NT; ++j) xrow[j] = token_row<K>(a.x, min(t0 + j * 8 + g, a.T - 1), a.n);
 
-    if constexpr (M != kFine) {
+    if constexpr (M <= 2) {
       auto fetch = [&](int c, Chunk<B, K, RT>& q) {
         const bool fast = xvec && c * 128 + 128 <= n;
         if constexpr (NT == 1) {
@@ -389,71 +364,128 @@ __global__ void __launch_bounds__(kWarps * 32)
         multiply(c, q, xvec && c * 128 + 128 <= n);
       }
     } else {
-      const bool g16 = gshift == 4;
-      for (int u0 = warp * 4; u0 < chunks * 4; u0 += kWarps * 4) {
-        const bool fast = xvec && u0 * 32 + 128 <= n;
-        uint32_t w[2 * RT][4][2], z[2 * RT][4];
-        float f[2 * RT][4];
-        Raw<K> x1[4];
+      // Groups of 32: lane t's 32 columns are the chunk's group t; of 16: its groups 2 t and
+      // 2 t + 1.  Every group's product is an instruction sequence of its own, with the other
+      // lanes' inputs at zero: four times the MMAs (the tensor pipe has room for them), with the
+      // loads and the unpacking of the wider groups.
+      constexpr int kOwn = M / 4;  // groups of a lane
+      struct Ahead {
+        uint32_t w[2 * RT][B];
+        uint32_t z[2 * RT][kOwn];
+        float f[2 * RT][kOwn];
+        Raw<K> x[4];
+      };
+      const char* cb = reinterpret_cast<const char*>(a.codes + row0 * words);
+      const char* sb = reinterpret_cast<const char*>(a.scales + row0 * G);
+      const char* zb = reinterpret_cast<const char*>(a.zeros + row0 * G);
+      uint32_t oc[2 * RT], og[2 * RT];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int unit = u0 + u;
-          if constexpr (NT == 1) load_raw<K>(xrow[0], unit * 32 + 8 * t, n, a.perm, fast, x1[u]);
-          const int gl = min((unit * 32 + 8 * t) >> gshift, G - 1);
-          const int g0 = min((unit * 32) >> gshift, G - 1);
+      for (int r = 0; r < 2 * RT; ++r) {
+        const int row = (int)min((int64_t)(8 * r + g), a.m - 1 - row0);
+        oc[r] = (uint32_t)(row * words + t * B) * 4;
+        og[r] = (uint32_t)(row * G);
+      }
+      auto fetch = [&](int c, bool clean, Ahead& q) {
+        if constexpr (NT == 1) {
+          const bool fast = clean || (xvec && c * 128 + 128 <= n);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            load_raw<K>(xrow[0], c * 128 + 32 * t + 8 * i, n, clean ? nullptr : a.perm, fast, q.x[i]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r) {
+          if (clean) load_words<B>(cb + (oc[r] + (uint32_t)c * 16 * B), q.w[r]);
+          else load_run<B>(cp[r], (c * 4 + t) * B, words, cvec, q.w[r]);
+#pragma unroll
+          for (int e = 0; e < kOwn; ++e) {
+            int gi = c * M + t * kOwn + e;
+            if (!clean) gi = min(gi, G - 1);
+            q.z[r][e] = __ldg(reinterpret_cast<const uint8_t*>(zb + (og[r] + gi)));
+            q.f[r][e] = __ldg(reinterpret_cast<const float*>(sb + (og[r] + gi) * 4));
+          }
+        }
+      };
+      auto multiply = [&](int c, const Ahead& q, bool fast) {
+        uint32_t pr[4][2 * RT][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          constexpr int kTop = B - 1;
+          const int w = (i * B) / 4, sh = 8 * ((i * B) % 4);
+          const int w1 = w + 1 < B ? w + 1 : kTop, w2 = w + 2 < B ? w + 2 : kTop;
 #pragma unroll
           for (int r = 0; r < 2 * RT; ++r) {
-            load_codes<B>(cp[r], unit, t, words, w[r][u][0], w[r][u][1]);
-            z[r][u] = __ldg(zp[r] + gl);
-            f[r][u] = __ldg(sp[r] + g0);
+            code_pairs<B>(__funnelshift_r(q.w[r][w], q.w[r][w1], sh),
+                          __funnelshift_r(q.w[r][w1], q.w[r][w2], sh), pair_other<B, kHalf>(),
+                          pr[i][r]);
+            const uint32_t zz = zero_pair<B, kHalf>(q.z[r][kOwn == 2 ? i >> 1 : 0]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pr[i][r][e] = pair_value<B, kHalf>(pr[i][r][e], zz);
           }
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int unit = u0 + u;
-          uint32_t pr[2 * RT][4];
-          float f1[2 * RT];
+        for (int j = 0; j < NT; ++j) {
+          uint32_t b[4][P][4];
 #pragma unroll
-          for (int r = 0; r < 2 * RT; ++r) {
-            code_pairs<B>(w[r][u][0], w[r][u][1], pair_other<B, kHalf>(), pr[r]);
-            const uint32_t zz = zero_pair<B, kHalf>(z[r][u]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pr[r][i] = pair_value<B, kHalf>(pr[r][i], zz);
-            f1[r] = g16 ? __ldg(sp[r] + min(unit * 2 + 1, G - 1)) : 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            uint32_t b[P][4];
+          for (int i = 0; i < 4; ++i) {
             if constexpr (NT == 1) {
-              input_pairs<K, P>(x1[u], b);
+              input_pairs<K, P>(q.x[i], b[i]);
             } else {
               Raw<K> x;
-              load_raw<K>(xrow[j], unit * 32 + 8 * t, n, a.perm, fast, x);
-              input_pairs<K, P>(x, b);
+              load_raw<K>(xrow[j], c * 128 + 32 * t + 8 * i, n, a.perm, fast, x);
+              input_pairs<K, P>(x, b[i]);
             }
-            // groups of 16: lanes 0, 1 of a quad hold the unit's first group, lanes 2, 3 its
-            // second; each half is multiplied with the other half's inputs at zero
+          }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (h == 1 && !g16) break;
-              const bool mine = !g16 || (t >> 1) == h;
+          for (int h = 0; h < 4; ++h) {
 #pragma unroll
-              for (int r = 0; r < RT; ++r) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int e = 0; e < kOwn; ++e) {
+              float d[RT][4];
+#pragma unroll
+              for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[r][i] = 0.f;
+#pragma unroll
+              for (int i = e * (4 / kOwn); i < (e + 1) * (4 / kOwn); ++i)
 #pragma unroll
                 for (int p = 0; p < P; ++p)
 #pragma unroll
-                  for (int e = 0; e < 4; e += 2)
-                    mma_16816<kHalf>(c, pr[2 * r][e], pr[2 * r + 1][e], pr[2 * r][e + 1],
-                                     pr[2 * r + 1][e + 1], mine ? b[p][e] : 0u,
-                                     mine ? b[p][e + 1] : 0u);
+                  for (int v = 0; v < 4; v += 2) {
+                    const uint32_t b0 = t == h ? b[i][p][v] : 0u, b1 = t == h ? b[i][p][v + 1] : 0u;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  acc[r][j][i] += (h ? f1[2 * r + (i >> 1)] : f[2 * r + (i >> 1)][u]) * c[i];
+                    for (int r = 0; r < RT; ++r)
+                      mma_16816<kHalf>(d[r], pr[i][2 * r][v], pr[i][2 * r + 1][v],
+                                       pr[i][2 * r][v + 1], pr[i][2 * r + 1][v + 1], b0, b1);
+                  }
+              const int src = (lane & ~3) | h;
+#pragma unroll
+              for (int r = 0; r < RT; ++r) {
+                const float fa = __shfl_sync(~0u, q.f[2 * r][e], src);
+                const float fb = __shfl_sync(~0u, q.f[2 * r + 1][e], src);
+                acc[r][j][0] += fa * d[r][0];
+                acc[r][j][1] += fa * d[r][1];
+                acc[r][j][2] += fb * d[r][2];
+                acc[r][j][3] += fb * d[r][3];
               }
             }
           }
         }
+      };
+      const int whole = xvec && cvec ? n / 128 : 0;
+      Ahead q[2];
+      if (warp < whole) fetch(warp, true, q[0]);
+      for (int c = warp; c < whole; c += 2 * kWarps) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int at = c + k * kWarps;
+          if (at < whole) {
+            if (at + kWarps < whole) fetch(at + kWarps, true, q[k ^ 1]);
+            multiply(at, q[k], true);
+          }
+        }
+      }
+      for (int c = whole + warp; c < chunks; c += kWarps) {
+        fetch(c, false, q[0]);
+        multiply(c, q[0], xvec && c * 128 + 128 <= n);
       }
     }
 #pragma unroll
@@ -508,7 +540,8 @@ void launch_mode(const LinearArgs& a, int xvec, cudaStream_t s) {
 }
 template <int B, LinearInput K>
 void launch_input(const LinearArgs& a, int xvec, cudaStream_t s) {
-  if (a.group == 16 || a.group == 32) launch_mode<B, K, kFine>(a, xvec, s);
+  if (a.group == 16) launch_mode<B, K, kEighths>(a, xvec, s);
+  else if (a.group == 32) launch_mode<B, K, kQuarters>(a, xvec, s);
   else if (a.group == 64) launch_mode<B, K, kHalves>(a, xvec, s);
   else launch_mode<B, K, kWhole>(a, xvec, s);
 }
