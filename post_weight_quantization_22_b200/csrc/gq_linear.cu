@@ -83,7 +83,11 @@ LinPlan plan_of(int64_t T, int64_t m, int64_t n, LinearInput kind, bool ordered)
   // the SMs once, where the tcgen05 kernel's fixed steps weigh more (48 tokens, 1024 x 4096, 2
   // bits: 9.0 us against 12.6; 64 tokens, 4096 x 4096: 32 against 18); not for fp32, whose parts
   // cost it three products (23 us against 16).
-  p.tc = T > 32 && (kind == kXFp32 || (m + 15) / 16 * ((T + 31) / 32) > kSMs);
+  // Rows of odd widths, and columns in an order, it reads one value at a time; from nine tokens on
+  // staging them for the tcgen05 kernel is faster (4096 x 4095: 16 tokens 29 us against 18, 32
+  // tokens 58 against 19).
+  const bool whole = n % 8 == 0 && !ordered;
+  p.tc = whole ? T > 32 && (kind == kXFp32 || (m + 15) / 16 * ((T + 31) / 32) > kSMs) : T > 8;
   p.P = kind == kXFp32 ? 3 : 1;
   // TMA takes rows whose length is a multiple of 16 bytes
   p.staged = kind != kXBf16 || ordered || n % 8 != 0;
