@@ -498,3 +498,80 @@ def test_half_a_chunk_at_the_end_of_many_tiles(bits, dtype):
         assert bool(((first.double() - ref).abs() <= 2.0 ** -24 * ref.abs() + 1.01 * sums * A).all())
         for _ in range(5):
             assert torch.equal(G.gq_linear(x, *dev, bits, group, y_dtype=torch.float32), first)
+
+
+def _check_on_gpu(y, x, w, xscale=None):
+    """check_linear's bounds, computed on the GPU in fp64."""
+    x, w = x.double(), torch.from_numpy(w).cuda()
+    ref, A = x @ w.T, x.abs() @ w.abs().T
+    if xscale is not None:
+        ref, A = ref * xscale.double()[:, None], A * xscale.double()[:, None]
+    n, half = x.shape[1], torch.finfo(y.dtype).eps / 2
+    sums = 3 * 256 * 2.0 ** -23 + (n / 16 + 18) * 2.0 ** -24
+    assert bool(((y.double() - ref).abs() <= half * ref.abs() + (1 + half) * sums * A + 1e-38).all())
+    rel = float((y.double() - ref).norm() / ref.norm())
+    assert rel <= half + 3 * 16 * 2.0 ** -23 + (n / 16 + 18) * 2.0 ** -24, rel
+
+
+@pytest.mark.parametrize("bits", range(2, 9))
+@pytest.mark.parametrize("group", GROUPS)
+def test_wide_layers(bits, group):
+    """Layers with rows enough for pairs of CTAs (3400 rows, 520 tokens) and for single CTAs that
+    take whole rows by TMA (2500 rows, 40 and 90 tokens), in every width and group."""
+    from post_weight_quantization_22_b200 import gq as G
+    for T, m, n in ((520, 3400, 256), (40, 2500, 320), (90, 2500, 192)):
+        c, s, z, w = layer_np(m, n, bits, group, bits + T, extreme=T == 90)
+        dev = to_cuda(c, s, z, bits)
+        for dtype in (torch.bfloat16, torch.float32):
+            x = _x(T, n, dtype, T)
+            buf, y = _guarded(T, m, torch.float32)
+            G.gq_linear(x, *dev, bits, group, y=y)
+            _check_on_gpu(y, x, w)
+            _whole(buf)
+        q, qs = _rows(T, n, T)
+        buf, y = _guarded(T, m, torch.bfloat16)
+        G.gq_linear_quantized(q, qs, *dev, bits, group, y=y)
+        _check_on_gpu(y, q, w, qs)
+        _whole(buf)
+
+
+def test_wide_layer_captured_and_on_two_streams():
+    """The tcgen05 kernels in a graph (their workspace in the graph's pool) and on two streams at
+    once."""
+    from post_weight_quantization_22_b200 import gq as G
+    bits, group, n = 4, 64, 512
+    c, s, z, w = layer_np(3000, n, bits, group, 2)
+    dev = to_cuda(c, s, z, bits)
+    xs = {T: _x(T, n, torch.bfloat16, T) for T in (100, 800)}
+    q, qs = _rows(800, n, 1)
+    ref = {T: G.gq_linear(x, *dev, bits, group) for T, x in xs.items()}
+    ref_q = G.gq_linear_quantized(q, qs, *dev, bits, group)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ya = G.gq_linear(xs[100], *dev, bits, group)
+        yb = G.gq_linear(xs[800], *dev, bits, group)
+        yc = G.gq_linear_quantized(q, qs, *dev, bits, group)
+    for _ in range(2):
+        graph.replay()
+        assert torch.equal(ya, ref[100]) and torch.equal(yb, ref[800]) and torch.equal(yc, ref_q)
+    st = (torch.cuda.Stream(), torch.cuda.Stream())
+    torch.cuda.synchronize()
+    got = [(T, G.gq_linear(xs[T], *dev, bits, group, stream=st[i % 2]))
+           for i, T in enumerate((100, 800) * 4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, ref[T]) for T, y in got)
+
+
+def test_workspace_status_after_a_product():
+    from post_weight_quantization_22_b200 import gq as G
+    c, s, z, w = layer_np(2500, 128, 4, 64, 2)
+    dev = to_cuda(c, s, z, 4)
+    x = _x(64, 128, torch.float32, 1)
+    ws = torch.full((G.gq_linear_workspace_size(64, 2500, 128, torch.float32),), 255,
+                    dtype=torch.uint8, device="cuda")
+    y = G.gq_linear(x, *dev, 4, 64, ws=ws)
+    assert G.gq_workspace_status(ws)[0] == 0
+    _check_on_gpu(y, x, w)
+    with pytest.raises(G.GQError) as e:
+        G.gq_linear(x, *dev, 4, 64, ws=ws[:-1])
+    assert e.value.code == 7
