@@ -168,7 +168,8 @@ cudaError_t launch_linear_rows(const LinearArgs& a, LinearInput kind, cudaStream
   if (a.T == 0) return cudaSuccess;
   const uintptr_t p = reinterpret_cast<uintptr_t>(a.x);
   // eight inputs of a token in one or two vector loads: rows have to start aligned
-  const int xvec = !a.perm && a.n % 8 == 0 && p % (kind == kXInt8 ? 8 : 16) == 0;
+  // (one token's row starts where the matrix does, whatever its width)
+  const int xvec = !a.perm && (a.n % 8 == 0 || a.T == 1) && p % (kind == kXInt8 ? 8 : 16) == 0;
   at_bits(a.bits, [&](auto b) {
     linear_rows_bits<decltype(b)::value>(a, kind, xvec, s);
     return cudaSuccess;

@@ -112,9 +112,14 @@ __device__ __forceinline__ const void* token_row(const void* x, int64_t t, int64
   return static_cast<const char*>(x) + t * n * size;
 }
 
-// B words in the widest loads that their size allows (16-byte aligned rows).
+// B words in the widest loads that their size allows (vec: rows are 16-byte aligned).
 template <int B>
-__device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[B]) {
+__device__ __forceinline__ void load_words(const char* p, bool vec, uint32_t (&w)[B]) {
+  if (B % 2 == 0 && !vec) {
+#pragma unroll
+    for (int i = 0; i < B; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    return;
+  }
   if constexpr (B % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < B / 4; ++i) {
@@ -137,7 +142,7 @@ __device__ __forceinline__ void load_words(const char* p, uint32_t (&w)[B]) {
 template <int B>
 __device__ __forceinline__ void load_run(const uint32_t* __restrict__ row, int w0, int words,
                                          bool vec, uint32_t (&w)[B]) {
-  if (vec && w0 + B <= words) return load_words<B>(reinterpret_cast<const char*>(row + w0), w);
+  if (vec && w0 + B <= words) return load_words<B>(reinterpret_cast<const char*>(row + w0), true, w);
 #pragma unroll
   for (int i = 0; i < B; ++i) w[i] = w0 + i < words ? __ldg(row + w0 + i) : 0u;
 }
@@ -273,11 +278,11 @@ __global__ void __launch_bounds__(kWarps * 32)
               for (int i = 0; i < 4; ++i)
                 acc[r][j][i] += q.f[2 * r + (i >> 1)][h] * part[h][r][j][i];
       };
-      // Whole chunks of aligned rows have no bounds to check, and every address is a base of the
+      // Whole chunks of aligned inputs have no bounds to check, and every address is a base of the
       // block plus a 32-bit offset.  They go to the warps in runs of four: lane t of a quad loads
       // the scales and zero points of the run's chunk t and hands them round (loaded by every
       // lane for every chunk they were half of the kernel's L1 wavefronts).
-      const int whole = xvec && cvec ? n / 128 : 0, runs = (whole + 3) / 4;
+      const int whole = xvec ? n / 128 : 0, runs = (whole + 3) / 4;
       {
         const char* cb = reinterpret_cast<const char*>(a.codes + row0 * words);
         const char* sb = reinterpret_cast<const char*>(a.scales + row0 * G);
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(kWarps * 32)
             }
           }
 #pragma unroll
-          for (int r = 0; r < 2 * RT; ++r) load_words<B>(cb + (oc[r] + (uint32_t)c * 16 * B), q.w[r]);
+          for (int r = 0; r < 2 * RT; ++r) load_words<B>(cb + (oc[r] + (uint32_t)c * 16 * B), cvec, q.w[r]);
         };
         Chunk<B, K, RT> q[2];
         if constexpr (NT == 1)
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         }
 #pragma unroll
         for (int r = 0; r < 2 * RT; ++r) {
-          if (clean) load_words<B>(cb + (oc[r] + (uint32_t)c * 16 * B), q.w[r]);
+          if (clean) load_words<B>(cb + (oc[r] + (uint32_t)c * 16 * B), cvec, q.w[r]);
           else load_run<B>(cp[r], (c * 4 + t) * B, words, cvec, q.w[r]);
 #pragma unroll
           for (int e = 0; e < kOwn; ++e) {
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(kWarps * 32)
           }
         }
       };
-      const int whole = xvec && cvec ? n / 128 : 0;
+      const int whole = xvec ? n / 128 : 0;
       Ahead q[2];
       if (warp < whole) fetch(warp, true, q[0]);
       for (int c = warp; c < whole; c += 2 * kWarps) {
