@@ -200,7 +200,8 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 
 // One lane of a converged warp.  Code behind it is known to run in one thread, so the tcgen05 and
 // TMA instructions in it are issued directly (behind a comparison of lane numbers each of them is
-// wrapped in a loop over the active lanes: 106 cycles per MMA measured, against 48 of the smallest MMA itself).
+// wrapped in a loop over the active lanes: 106 cycles per MMA measured, against 48 of the smallest
+// MMA itself).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
