@@ -18,14 +18,15 @@ class QuantizedLinear:
     ``codes`` / ``scales`` / ``zeros`` as gq_quantize_layer writes them for a clamped or clip-free
     layer with uniform spacing.  ``perm`` is the column order of a layer quantized in one: with
     groups the codes are repacked in that order here, once (without groups they keep their
-    columns).  The tensors are used as they are, not copied, except for that repacking.
+    columns).  The tensors are used as they are, not copied, except for that repacking, which is
+    enqueued on ``stream`` (default: the current one) and belongs to it.
     """
 
-    def __init__(self, codes, scales, zeros, n: int, cfg: G.QuantCfg, perm=None):
+    def __init__(self, codes, scales, zeros, n: int, cfg: G.QuantCfg, perm=None, stream=None):
         if cfg.clip == "unbounded" or cfg.spacing != "uniform":
             raise ValueError("packed codes of uniform spacing only (no unbounded codes, no ZSIC)")
         if perm is not None and cfg.group_size:
-            codes = G.gq_order_codes(codes, n, cfg.bits, perm)
+            codes = G.gq_order_codes(codes, n, cfg.bits, perm, stream=stream)
         else:
             perm = None
         self.codes, self.scales, self.zeros, self.perm = codes, scales, zeros, perm
@@ -133,16 +134,17 @@ class LayerQuantizer:
         self.quantize(W, stream=stream)
         return self.result()
 
-    def linear(self) -> QuantizedLinear:
+    def linear(self, stream=None) -> QuantizedLinear:
         """The quantized layer as one that runs, on this quantizer's own result buffers (the next
-        ``quantize`` writes them; an ordered layer with groups is repacked and keeps its codes)."""
+        ``quantize`` writes them; an ordered layer with groups is repacked, on ``stream``, and
+        keeps its codes)."""
         return QuantizedLinear(self.codes, self.scales, self.zeros, self.n, self.cfg,
-                               self.perm if self.order else None)
+                               self.perm if self.order else None, stream)
 
     def output(self, X: torch.Tensor, y=None, stream=None) -> torch.Tensor:
         """X W^T with the quantized weights, in X's type: the calibration input of what follows
         this layer, as the quantized model will produce it."""
-        return self.linear()(X, y=y, stream=stream)
+        return self.linear(stream)(X, y=y, stream=stream)
 
     def status(self):
         """(prepare status, quantize status, ladder rounds); synchronizes."""
