@@ -432,7 +432,7 @@ def _elsewhere(device: int, stream) -> bool:
     return stream is not None or device != torch.cuda.current_device()
 
 
-class _On:
+class on_stream:
     """The tensors' device and the call's stream made current."""
 
     def __init__(self, device: int, stream):
@@ -490,7 +490,7 @@ def gq_order_codes(codes: torch.Tensor, n: int, bits: int, perm: torch.Tensor, o
         raise ValueError(f"bits: 2 to 8, got {bits}")
     (m, _), device = _rows(codes, "codes")
     if _elsewhere(device, stream):
-        with _On(device, stream):
+        with on_stream(device, stream):
             return gq_order_codes(codes, n, bits, perm, out)
     _need_on(codes, torch.int32, (m, n_words(n, bits)), device, "codes")
     _need_on(perm, torch.int32, (n,), device, "perm")
@@ -522,7 +522,7 @@ def gq_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros:
     ``y_dtype`` (default: x's).  ``perm``: the codes are in processing order (gq_order_codes)."""
     (T, n), device = _rows(x, "x")
     if _elsewhere(device, stream):
-        with _On(device, stream):
+        with on_stream(device, stream):
             return gq_linear(x, codes, scales, zeros, bits, group_size, perm, y, y_dtype, ws)
     xc = _dtype_code(x)
     m = _layer_args(codes, scales, zeros, n, bits, group_size, perm, device)
@@ -548,7 +548,7 @@ def gq_linear_quantized(q: torch.Tensor, qscale: torch.Tensor, codes: torch.Tens
     """gq_linear on 8-bit rows: x = qscale[:, None] * q (q int8 T x n, qscale fp32 T)."""
     (T, n), device = _rows(q, "q")
     if _elsewhere(device, stream):
-        with _On(device, stream):
+        with on_stream(device, stream):
             return gq_linear_quantized(q, qscale, codes, scales, zeros, bits, group_size, perm, y,
                                        y_dtype, ws)
     _need_on(q, torch.int8, (T, n), device, "q")
@@ -577,7 +577,7 @@ def gq_rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6,
     where not written."""
     (T, n), device = _rows(x, "x")
     if _elsewhere(device, stream):
-        with _On(device, stream):
+        with on_stream(device, stream):
             return gq_rmsnorm_quantize(x, gamma, eps, residual, sum, y, q, qscale)
     xc, gc, xt, shape = _dtype_code(x), _dtype_code(gamma), x.dtype, (T, n)
     _need_on(gamma, gamma.dtype, (n,), device, "gamma")

@@ -295,13 +295,15 @@ class BlockQuantizer:
         names = [l[0] for l in self.layers if l[3] == key]
         if not names:
             raise ValueError(f"no layer reads {key!r}")
+        if stream is not None:  # what is allocated here belongs to the call's stream too
+            with G.on_stream(x.get_device(), stream):
+                return self.forward(key, x, gamma, residual, eps, quantized)
         y = None if quantized else torch.empty_like(x)
-        r = G.gq_rmsnorm_quantize(x, gamma, eps, residual=residual, y=y, stream=stream)
+        r = G.gq_rmsnorm_quantize(x, gamma, eps, residual=residual, y=y)
         out = {"sum": r["sum"]}
         for name in names:
             f = self.linear(name)
-            out[name] = (f(r["q"], r["qscale"], y_dtype=x.dtype, stream=stream) if quantized
-                         else f(r["y"], stream=stream))
+            out[name] = f(r["q"], r["qscale"], y_dtype=x.dtype) if quantized else f(r["y"])
         return out
 
     def run(self, Ws: dict, Xs: dict, names=None, stream=None) -> dict:

@@ -44,3 +44,47 @@ def test_output_repacks_on_its_stream(calls):
     lq.linear(stream)
     lq.linear()
     assert [(c[0], c[2]) for c in calls] == [("order", stream), ("order", None)]
+
+
+@pytest.mark.parametrize("quantized", (True, False))
+def test_forward_allocates_on_its_stream(monkeypatch, quantized):
+    """What BlockQuantizer.forward allocates for itself is allocated on the stream that its calls
+    run on."""
+    from post_weight_quantization_22_b200 import gq as G
+    from post_weight_quantization_22_b200.pipeline import BlockQuantizer
+    side = types.SimpleNamespace(device=types.SimpleNamespace(index=-1))  # a CPU tensor's get_device()
+    current, seen = [None], []
+
+    class Use:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.stream
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    def norm(x, gamma, eps=1e-6, residual=None, sum=None, y=None, q=None, qscale=None, stream=None):
+        seen.append(("norm", current[0] if stream is None else stream))
+        return dict(sum=None, y=y, q=x, qscale=gamma)
+
+    def product(*args, stream=None, **kw):
+        stream = args[-1] if stream is None and len(args) > 9 else stream
+        seen.append(("product", current[0] if stream is None else stream))
+        return args[0]
+
+    def empty_like(x, **kw):
+        seen.append(("alloc", current[0]))
+        return torch.zeros_like(x)
+
+    bq = BlockQuantizer((("q", 8, 64, "attn"), ("k", 8, 64, "attn")), G.QuantCfg(bits=4),
+                        device="cpu", max_tokens=16)
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(torch, "empty_like", empty_like)
+    monkeypatch.setattr(G, "gq_rmsnorm_quantize", norm)
+    monkeypatch.setattr(G, "gq_linear", product)
+    monkeypatch.setattr(G, "gq_linear_quantized", product)
+    bq.forward("attn", torch.zeros(3, 64), torch.ones(64), quantized=quantized, stream=side)
+    assert [s[0] for s in seen] == ([] if quantized else ["alloc"]) + ["norm", "product", "product"]
+    assert all(s[1] is side for s in seen)

@@ -40,3 +40,45 @@ def test_output_on_a_side_stream(T):
     side.synchronize()
     w = _weights(lq.codes, lq.scales, lq.zeros, n, 4, 64, lq.perm)
     check_linear(y, X[:T].double().cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("T", (3, 200))
+def test_forward_on_a_side_stream(T):
+    """BlockQuantizer.forward in both modes on a stream of its own, the current stream busy and
+    taking memory back into use right behind the call; every output against the formula."""
+    from post_weight_quantization_22_b200 import gq as G
+    from post_weight_quantization_22_b200.pipeline import BlockQuantizer
+    layers = (("q", 128, 256, "attn"), ("k", 64, 256, "attn"), ("v", 64, 256, "attn"))
+    bq = BlockQuantizer(layers, G.QuantCfg(bits=3, group_size=64))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Ws = {name: (0.02 * torch.randn(m, n, generator=g, device="cuda")).bfloat16()
+          for name, m, n, _ in layers}
+    bq.run(Ws, {"attn": torch.randn(400, 256, generator=g, device="cuda").bfloat16()})
+    gamma = (1 + 0.1 * torch.randn(256, generator=g, device="cuda")).bfloat16()
+    x, res = (torch.randn(T, 256, generator=g, device="cuda").bfloat16() for _ in range(2))
+    h, v, q, qs = norm_np(x.double().cpu().numpy(), res.double().cpu().numpy(),
+                          gamma.double().cpu().numpy(), 1e-6, torch.bfloat16)
+    side = torch.cuda.Stream()
+    for quantized in (True, False):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(BUSY)
+        out = bq.forward("attn", x, gamma, residual=res, quantized=quantized, stream=side)
+        for _ in range(8):
+            torch.full_like(x, float("nan"))
+        side.synchronize()
+        assert np.array_equal(out["sum"].double().cpu().numpy(), h)
+        for name, _, n, _ in layers:
+            o = bq.out[name]
+            w = _weights(o["codes"], o["scales"], o["zeros"], n, 3, 64)
+            if quantized:
+                check_linear(out[name], q.astype(np.float64), w, qs.astype(np.float32).astype(np.float64))
+            else:
+                # the norm's rows in bf16 are off by half a step at most (and 2^-23: they are
+                # rounded from fp32), the product of them as check_linear says: sums of at most
+                # 3 * 256 truncated additions a run, n / 16 + 18 of 2^-24, half a step of y
+                ref, A = v @ w.T, np.abs(v) @ np.abs(w).T
+                half = torch.finfo(torch.bfloat16).eps / 2
+                sums = 3 * 256 * 2.0 ** -23 + (n / 16 + 18) * 2.0 ** -24
+                off = (half + 2.0 ** -23 + (1 + half) * sums) * A
+                got = out[name].double().cpu().numpy()
+                assert np.all(np.abs(got - ref) <= half * (np.abs(ref) + off) + off + 1e-38)
