@@ -17,9 +17,10 @@ class QuantizedLinear:
 
     ``codes`` / ``scales`` / ``zeros`` as gq_quantize_layer writes them for a clamped or clip-free
     layer with uniform spacing.  ``perm`` is the column order of a layer quantized in one: with
-    groups the codes are repacked in that order here, once (without groups they keep their
-    columns).  The tensors are used as they are, not copied, except for that repacking, which is
-    enqueued on ``stream`` (default: the current one) and belongs to it.
+    groups the codes are repacked in that order here, once, and scales, zeros and perm are copied
+    beside them, so that all four stay one layer whatever is written to the tensors later (without
+    groups the codes keep their columns).  Repacking and copies are enqueued on ``stream``
+    (default: the current one) and belong to it.  Otherwise the tensors are used as they are.
     """
 
     def __init__(self, codes, scales, zeros, n: int, cfg: G.QuantCfg, perm=None, stream=None):
@@ -27,6 +28,8 @@ class QuantizedLinear:
             raise ValueError("packed codes of uniform spacing only (no unbounded codes, no ZSIC)")
         if perm is not None and cfg.group_size:
             codes = G.gq_order_codes(codes, n, cfg.bits, perm, stream=stream)
+            with torch.cuda.stream(stream):
+                scales, zeros, perm = scales.clone(), zeros.clone(), perm.clone()
         else:
             perm = None
         self.codes, self.scales, self.zeros, self.perm = codes, scales, zeros, perm
@@ -135,9 +138,9 @@ class LayerQuantizer:
         return self.result()
 
     def linear(self, stream=None) -> QuantizedLinear:
-        """The quantized layer as one that runs, on this quantizer's own result buffers (the next
-        ``quantize`` writes them; an ordered layer with groups is repacked, on ``stream``, and
-        keeps its codes)."""
+        """The quantized layer as one that runs, on this quantizer's own result buffers, which the
+        next ``quantize`` writes; an ordered layer with groups is a copy of them (repacked, on
+        ``stream``) and stays as it is."""
         return QuantizedLinear(self.codes, self.scales, self.zeros, self.n, self.cfg,
                                self.perm if self.order else None, stream)
 

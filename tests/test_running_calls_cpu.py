@@ -88,3 +88,18 @@ def test_forward_allocates_on_its_stream(monkeypatch, quantized):
     bq.forward("attn", torch.zeros(3, 64), torch.ones(64), quantized=quantized, stream=side)
     assert [s[0] for s in seen] == ([] if quantized else ["alloc"]) + ["norm", "product", "product"]
     assert all(s[1] is side for s in seen)
+
+
+def test_a_kept_ordered_layer_is_a_copy(calls):
+    """Grids and order of a repacked layer are its own, as its codes are; a layer that is not
+    repacked uses the quantizer's buffers."""
+    lq = _ordered_quantizer()
+    layer = lq.linear()
+    for name in ("codes", "scales", "zeros", "perm"):
+        a, b = getattr(layer, name), getattr(lq, name)
+        assert a.data_ptr() != b.data_ptr() and torch.equal(a, b), name
+    plain = _ordered_quantizer(order=None).linear()
+    assert plain.perm is None
+    lq = _ordered_quantizer(group=0)
+    layer = lq.linear()
+    assert layer.perm is None and layer.codes is lq.codes and layer.scales is lq.scales

@@ -82,3 +82,21 @@ def test_forward_on_a_side_stream(T):
                 off = (half + 2.0 ** -23 + (1 + half) * sums) * A
                 got = out[name].double().cpu().numpy()
                 assert np.all(np.abs(got - ref) <= half * (np.abs(ref) + off) + off + 1e-38)
+
+
+def test_a_kept_ordered_layer_stays_what_it_was():
+    """A repacked layer after the quantizer has written another order, other grids and codes."""
+    from post_weight_quantization_22_b200 import gq as G, synth
+    from post_weight_quantization_22_b200.pipeline import LayerQuantizer
+    m, n = 96, 256
+    W, X, _ = synth.workload("q_proj_4096x4096", m=m, n=n, T=300)
+    W, X = W.cuda().contiguous(), X.cuda().contiguous()
+    lq = LayerQuantizer(m, n, G.QuantCfg(bits=4, group_size=64), order="act")
+    lq.run(W, X)
+    layer, w = lq.linear(), _weights(lq.codes, lq.scales, lq.zeros, n, 4, 64, lq.perm)
+    first = layer(X)
+    check_linear(first, X.double().cpu().numpy(), w)
+    perm = lq.perm.clone()
+    lq.run((3 * W.flip(1)).contiguous(), X.flip(1).contiguous())
+    assert not torch.equal(lq.perm, perm)
+    assert torch.equal(layer(X), first)
