@@ -185,7 +185,12 @@ cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaS
   const bool aligned = p.staged || reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
   const int64_t rows_total = (int64_t)p.P * a.T;
   // (tile coordinates are 32-bit)
-  if (!p.tc || !aligned || rows_total > INT32_MAX - 1024) return launch_linear_rows(a, kind, s);
+  if (!p.tc) return launch_linear_rows(a, kind, s);
+  if (!aligned || rows_total > INT32_MAX - 1024) {
+    // (this call has a workspace, and the warp-level kernel has no status to write)
+    const cudaError_t e = cudaMemsetAsync(&static_cast<WsHeader*>(ws)->status, 0, sizeof(int), s);
+    return e != cudaSuccess ? e : launch_linear_rows(a, kind, s);
+  }
   const void* xt = a.x;
   int64_t ld = a.n, cols = a.n;
   if (p.staged) {

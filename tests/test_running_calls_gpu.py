@@ -100,3 +100,22 @@ def test_a_kept_ordered_layer_stays_what_it_was():
     lq.run((3 * W.flip(1)).contiguous(), X.flip(1).contiguous())
     assert not torch.equal(lq.perm, perm)
     assert torch.equal(layer(X), first)
+
+
+@pytest.mark.parametrize("T", (64, 300))
+def test_status_word_of_a_misaligned_matrix(T):
+    """A bf16 matrix off the 16-byte boundaries that tensor maps need: the call asks for a workspace
+    as for an aligned one and leaves its status word clean."""
+    from post_weight_quantization_22_b200 import gq as G
+    m, n, bits, group = 4096, 256, 4, 64
+    c, s, z, w = layer_np(m, n, bits, group, T)
+    dev = to_cuda(c, s, z, bits)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T * n + 1, generator=g, device="cuda").bfloat16()[1:].view(T, n)
+    assert x.data_ptr() % 16 == 2
+    need = G.gq_linear_workspace_size(T, m, n, torch.bfloat16)
+    assert need > 0
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    y = G.gq_linear(x, *dev, bits, group, y_dtype=torch.float32, ws=ws)
+    check_linear(y, x.double().cpu().numpy(), w)
+    assert G.gq_workspace_status(ws)[0] == 0
