@@ -471,13 +471,17 @@ gq_status gq_rmsnorm_quantize(const void* d_x, const void* d_residual, gq_dtype 
 /*
  * Test setting of the bounded device waits, for tests of the timeout path (process-wide, read
  * when a call is enqueued; default off).  poll_limit > 0 replaces the poll budget of the
- * factor's per-pivot waits in gq_prepare_hinv(_ordered) (0 restores the default of about 2^26
- * polls, well over a second); withhold_arrival = 1 makes the factor's leaf kernel withhold one
+ * factor's per-pivot waits in gq_prepare_hinv(_ordered) and of the waits of gq_linear and
+ * gq_linear_quantized, where less than 4096 counts as 4096 (0 restores the default of about 2^26
+ * polls, well over a second).  withhold_arrival = 1 makes the factor's leaf kernel withhold one
  * thread's first barrier arrival, so that every wait of that phase runs out: the kernel records
  * GQ_ERR_TIMEOUT in the workspace and returns (no copy or tensor-core operation is in flight in
- * that kernel), and the call's U is undefined.  withhold_arrival must be 0 or 1.  The setting is
- * part of the key under which a call's launch sequence is cached, so calls made under it never
- * replay as clean calls.
+ * that kernel), and the call's U is undefined.  In the tcgen05 kernel of the products (calls that
+ * need a workspace, n > 64) the first CTA withholds the arrival for its second stage of 64
+ * columns: the kernel waits for its copies and products in flight, frees its tensor memory,
+ * records GQ_ERR_TIMEOUT and returns, and the call's y is undefined.  withhold_arrival must be 0
+ * or 1.  The setting is part of the key under which a call's launch sequence is cached, so calls
+ * made under it never replay as clean calls.
  */
 gq_status gq_debug_wait_test(uint32_t poll_limit, int withhold_arrival);
 

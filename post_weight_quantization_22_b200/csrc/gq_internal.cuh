@@ -125,7 +125,8 @@ constexpr int kBlock = 128;  // columns per GPTQ block (lazy-update rank)
 void count_launches(long k);
 
 // Test setting of the bounded waits (gq_debug_wait_test): the poll budget of the factor leaf
-// kernel's per-pivot waits and whether that kernel withholds one thread's first arrival.
+// kernel's per-pivot waits and of the tcgen05 products' waits, and whether those kernels withhold
+// one thread's first arrival.
 struct WaitTest {
   uint32_t polls;
   int withhold;

@@ -230,6 +230,9 @@ cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaS
   // (a pair's in whole packed chunks: what lies behind the last column reads as zero)
   t.stages = pair ? (int)((a.n + 127) / 128 * 2) : (int)((a.n + kCols - 1) / kCols);
   t.hdr = static_cast<WsHeader*>(ws);
+  t.wait = wait_test();
+  // (no budget so short that a role gives up before copies that were just issued can have landed)
+  t.wait.polls = t.wait.polls < 4096 ? 4096 : t.wait.polls;
   t.gshift = a.group ? __builtin_ctz((unsigned)a.group) : 31;
   t.dmask = a.group ? a.group / 16 - 1 : 15;
   t.groups = a.group ? (int)((a.n + a.group - 1) / a.group) : 1;

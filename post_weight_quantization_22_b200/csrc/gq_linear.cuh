@@ -19,6 +19,7 @@ struct LinTcArgs {
   int dmask;         // 16-column steps per accumulator period (a power of two) - 1
   int groups;        // groups of a row
   WsHeader* hdr;
+  WaitTest wait;     // budget of the kernel's waits (test setting)
 };
 
 // The kernels for codes of B bits.  rows: the warp-level product (xvec: inputs allow vector

@@ -50,10 +50,15 @@ constexpr int lin_chunks(int B, int P) {
   return fit < 8 ? fit : 8;
 }
 
+// What a loading thread waits at its end for each of its last copies: they take microseconds, and
+// 2^18 looks at a barrier 20 ms, also where the phase stays open because another role has given up.
+constexpr uint32_t kDrainPolls = 1u << 18;
+constexpr long long kDrainCycles = 4000000;  // the same for a thread that cannot look: 2 ms
 
-// Waits as mbar_wait, but also gives up when another role of the CTA has.
-__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, volatile int* fail) {
-  for (uint32_t i = 0; i < tc::kDefaultPolls; ++i) {
+// Waits for at most `polls` looks, and gives up when another role of the CTA has.
+__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, volatile int* fail,
+                                             uint32_t polls) {
+  for (uint32_t i = 0; i < polls; ++i) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     if ((i & 1023) == 1023 && *fail) return false;
   }
@@ -61,8 +66,9 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, vol
   return false;
 }
 // The same for a whole warp, with one answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
-  return __all_sync(~0u, wait_or_fail(bar, parity, fail));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* fail,
+                                          uint32_t polls) {
+  return __all_sync(~0u, wait_or_fail(bar, parity, fail, polls));
 }
 
 __device__ __forceinline__ void fma2(uint64_t& acc, float a, float b, uint64_t s) {
@@ -223,6 +229,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t S = cluster_size(), rank = cluster_rank();
   const int tile0 = (int)(blockIdx.x / S), tstep = (int)(gridDim.x / S);
   const int N = a.N;
+  const uint32_t polls = a.wait.polls;
   // this CTA's stages: all, or its share of a tile that a cluster splits (in runs of 256 columns,
   // the longest period)
   const int runs = (a.stages + 3) / 4;
@@ -284,15 +291,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         int i = 0, s = 0;
         uint32_t ph = 1;
         bool ok = true;
+        // (test setting: the first CTA withholds its second arrival, so that this stage never fills
+        // and every role runs out of looks, behind one stage's MMAs and with the ring loaded)
+        const bool held = a.wait.withhold && blockIdx.x == 0;
         for (int tile = tile0; tile < a.tiles && ok; tile += tstep) {
           const int t0 = (int)(tok_of(tile) + (kPair ? 128 * rank : 0));
           for (int st = 0; st < ns; ++st, ++i) {
-            if (i >= kStages && !wait_or_fail(&empty[s], ph, fail)) {
+            if (i >= kStages && !wait_or_fail(&empty[s], ph, fail, polls)) {
               ok = false;
               break;
             }
-            if (!kPair || rank == 0)
-              tc::mbar_arrive_expect_tx(&full[s], (uint32_t)((kPair ? 2 : 1) * P * rows * 128));
+            if (!kPair || rank == 0) {
+              const uint32_t bytes = (uint32_t)((kPair ? 2 : 1) * P * rows * 128);
+              if (held && i == 1) tc::mbar_expect_tx(&full[s], bytes);
+              else tc::mbar_arrive_expect_tx(&full[s], bytes);
+            }
             uint8_t* dst = base + s * kStage + kTile;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
@@ -308,11 +321,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
           }
         }
-        // After a failure no copy may be in flight when the CTAs end: the first CTA's barriers
-        // count both CTAs' bytes, and the pair ends together.
-        if (!ok && (!kPair || rank == 0))
+        // No copy may be in flight when the CTAs end, whichever role has given up (where none has,
+        // the other roles wait for the same phases): the first CTA's barriers count both CTAs'
+        // bytes, and the pair ends together.  The second CTA cannot look at them; where it gives
+        // up, it leaves its last copies their time.
+        if (!kPair || rank == 0) {
           for (int j = max(0, i - kStages); j < i; ++j)
-            tc::mbar_wait(&full[j % kStages], (j / kStages) & 1);
+            tc::mbar_wait_polls(&full[j % kStages], (j / kStages) & 1, kDrainPolls);
+        } else if (!ok) {
+          const long long t = clock64();
+          while (clock64() - t < kDrainCycles) {}
+        }
       }
     } else if (kPair && warp == 3) {
       if (tc::elect_one()) {
@@ -323,7 +342,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int tile = tile0; tile < a.tiles && ok; tile += tstep) {
           const int row = (int)row_of(tile);
           for (int c = 0; 2 * c < ns; ++c, ++i) {
-            if (i >= kChunks && !wait_or_fail(&c_empty[s], ph, fail)) {
+            if (i >= kChunks && !wait_or_fail(&c_empty[s], ph, fail, polls)) {
               ok = false;
               break;
             }
@@ -335,9 +354,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
           }
         }
-        if (!ok)
-          for (int j = max(0, i - kChunks); j < i; ++j)
-            tc::mbar_wait(&c_full[j % kChunks], (j / kChunks) & 1);
+        for (int j = max(0, i - kChunks); j < i; ++j)
+          tc::mbar_wait_polls(&c_full[j % kChunks], (j / kChunks) & 1, kDrainPolls);
       }
     } else if (warp == 1 && (!kPair || rank == 0)) {
       if (tc::elect_one()) {
@@ -362,7 +380,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int tile = tile0; tile < a.tiles && ok; tile += tstep) {
           int step = 0;
           for (int st = 0; st < ns; ++st) {
-            if (!seen && !wait_or_fail(&full[s], ph, fail)) {
+            if (!seen && !wait_or_fail(&full[s], ph, fail, polls)) {
               ok = false;
               break;
             }
@@ -372,7 +390,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if (dmask >= 3) {  // a period is one or more stages
               const bool first = (step & dmask) == 0;
               if (first && period >= 2 && !free_seen)
-                ok = wait_or_fail(&t_empty[period & 1], ((period >> 1) - 1) & 1, fail);
+                ok = wait_or_fail(&t_empty[period & 1], ((period >> 1) - 1) & 1, fail, polls);
               if (!ok) break;
               seen = tc::mbar_test_wait(&full[s_next], ph_next);
               tc::fence_after_sync();
@@ -395,7 +413,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               for (int k = 0; k < 4; ++k) {
                 const bool first = (step & dmask) == 0;
                 if (first && period >= 2)
-                  ok = ok && wait_or_fail(&t_empty[period & 1], ((period >> 1) - 1) & 1, fail);
+                  ok = ok && wait_or_fail(&t_empty[period & 1], ((period >> 1) - 1) & 1, fail, polls);
                 if (!ok) break;
                 tc::fence_after_sync();
                 const uint32_t d = tmem + (period & 1) * kN;
@@ -494,12 +512,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     while (tile < a.tiles) {
       const int cc = chunk0 + (st >> 1), cs = cc % kChunks;
       if constexpr (kPair) {
-        if (!warp_wait(&c_full[cs], (cc / kChunks) & 1, fail)) break;
+        if (!warp_wait(&c_full[cs], (cc / kChunks) & 1, fail, polls)) break;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           load_unit_smem<B>(cring + cs * kChunkBytes, r_in + 16 * i, (st & 1) * 2 + u2, w[i]);
       }
-      if (use > 0 && !warp_wait(&empty[s], (use - 1) & 1, fail)) break;
+      if (use > 0 && !warp_wait(&empty[s], (use - 1) & 1, fail, polls)) break;
       uint8_t* tilep = base + s * kStage;
       int next = tile;
       st += 2;
@@ -553,7 +571,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       for (int p = 0; p < periods; ++p, ++pt) {
         const float s = s_next;
         if (!grid1 && p + 1 < periods) s_next = __ldg(sp + min(gfirst + p + 1, G - 1));
-        if (!warp_wait(&t_full[pt & 1], (pt >> 1) & 1, fail)) {
+        if (!warp_wait(&t_full[pt & 1], (pt >> 1) & 1, fail, polls)) {
           ok = false;
           break;
         }

@@ -119,3 +119,38 @@ def test_status_word_of_a_misaligned_matrix(T):
     y = G.gq_linear(x, *dev, bits, group, y_dtype=torch.float32, ws=ws)
     check_linear(y, x.double().cpu().numpy(), w)
     assert G.gq_workspace_status(ws)[0] == 0
+
+
+@pytest.mark.parametrize("dtype", (torch.bfloat16, torch.float32))
+@pytest.mark.parametrize("form,T,m,n", (("one CTA a tile", 64, 4096, 256),
+                                        ("a cluster a tile", 64, 2048, 2048),
+                                        ("pairs of CTAs", 1024, 2560, 512)))
+def test_a_wait_of_the_product_runs_out(form, T, m, n, dtype):
+    """With the test setting the first CTA never announces its second stage: every wait that needs
+    it gives up, the kernel returns, the status word says GQ_ERR_TIMEOUT, and the next call on the
+    same workspace is clean and right."""
+    import time
+    from post_weight_quantization_22_b200 import gq as G
+    bits, group = 4, 64
+    c, s, z, w = layer_np(m, n, bits, group, 11)
+    dev = to_cuda(c, s, z, bits)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, n, generator=g, device="cuda").to(dtype)
+    ws = torch.zeros(G.gq_linear_workspace_size(T, m, n, dtype), dtype=torch.uint8, device="cuda")
+    y = torch.empty(T, m, device="cuda")
+    torch.cuda.synchronize()
+    G.gq_debug_wait_test(16384, True)
+    try:
+        t0 = time.perf_counter()
+        G.gq_linear(x, *dev, bits, group, y=y, ws=ws)
+        torch.cuda.synchronize()
+        elapsed = time.perf_counter() - t0
+    finally:
+        G.gq_debug_wait_test()
+    print(f"{form}: {elapsed:.3f} s")
+    assert G.gq_workspace_status(ws)[0] == 5           # GQ_ERR_TIMEOUT
+    assert elapsed < 30.0
+    G.gq_linear(x, *dev, bits, group, y=y, ws=ws)
+    assert G.gq_workspace_status(ws)[0] == 0
+    rows = np.r_[0:8, T - 8:T]
+    check_linear(y[rows], x.double().cpu().numpy()[rows], w)
