@@ -384,7 +384,7 @@ gq_status gq_huffman_encode(const int32_t* d_codes, int64_t count, uint64_t* d_s
  * outliers are not part of the packed stream.)  A workspace serves one call at a time: calls
  * whose work may overlap need one each.  After a call that needed a workspace its status word
  * (gq_workspace_status) holds GQ_OK, or GQ_ERR_TIMEOUT if a bounded device wait ran out (d_y is
- * then undefined).
+ * then undefined); gq_linear_status says the same of all calls on a device.
  */
 
 /*
@@ -443,6 +443,14 @@ gq_status gq_linear_quantized(const int8_t* d_q, const float* d_qscale, int64_t 
                               const uint8_t* d_zeros, int bits, int group_size,
                               const int32_t* d_perm, void* d_y, gq_dtype y_dtype, void* d_ws,
                               size_t ws_bytes, gq_stream_t stream);
+
+/*
+ * Synchronize `stream` and return GQ_ERR_TIMEOUT if a bounded wait ran out in any gq_linear or
+ * gq_linear_quantized call that this device (the current one) finished since the last look, else
+ * GQ_OK; then clear it.  For programs that do not keep the calls' workspaces, and for replayed
+ * graphs; not to be called while `stream` is being captured.
+ */
+gq_status gq_linear_status(gq_stream_t stream);
 
 /*
  * Root-mean-square norm of T rows with the residual's addition, and the normalised rows in 8

@@ -453,6 +453,19 @@ gq_status gq_linear_quantized(const int8_t* d_q, const float* d_qscale, int64_t 
   return linear_common(a, kXInt8, y_dtype, d_ws, ws_bytes, stream);
 }
 
+gq_status gq_linear_status(gq_stream_t stream) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return GQ_ERR_CUDA;
+  WsHeader* at = nullptr;
+  {
+    std::lock_guard<std::mutex> lk(g_init_mu);
+    if (g_linear_done[dev]) at = linear_device_status(dev);
+  }
+  if (!at)  // no call has waited on this device
+    return cudaStreamSynchronize((cudaStream_t)stream) == cudaSuccess ? GQ_OK : GQ_ERR_CUDA;
+  return gq_workspace_status(at, nullptr, stream);
+}
+
 gq_status gq_rmsnorm_quantize(const void* d_x, const void* d_residual, gq_dtype x_dtype,
                               const void* d_gamma, gq_dtype gamma_dtype, int64_t T, int64_t n,
                               double eps, void* d_sum, void* d_y, int8_t* d_q, float* d_qscale,

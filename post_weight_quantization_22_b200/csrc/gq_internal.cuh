@@ -231,10 +231,11 @@ struct LinearArgs {
 };
 // The product on the warp-level tensor cores, for few tokens (correct for any T).
 cudaError_t launch_linear_rows(const LinearArgs& a, LinearInput kind, cudaStream_t s);
-// The product by the kernel that fits its sizes (gq_linear_tc.cu); ws of linear_ws_bytes.
+// The product by the kernel that fits its sizes; ws of linear_ws_bytes.
 size_t linear_ws_bytes(int64_t T, int64_t m, int64_t n, LinearInput kind, bool ordered);
 cudaError_t linear_init_attributes();
 cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaStream_t s);
+WsHeader* linear_device_status(int dev);  // device memory; null before linear_init_attributes
 cudaError_t launch_order_codes(const uint32_t* codes, int64_t m, int64_t n, int bits,
                                const int32_t* perm, uint32_t* out, cudaStream_t s);
 

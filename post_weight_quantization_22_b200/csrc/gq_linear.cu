@@ -150,7 +150,12 @@ size_t linear_ws_bytes(int64_t T, int64_t m, int64_t n, LinearInput kind, bool o
 namespace {
 // clusters of 2^i CTAs that a device runs at once (written once per device, before its first call)
 int g_clusters[128][4];
+// every device's status of all products, and where it lies
+__device__ WsHeader g_device_status;
+WsHeader* g_device_status_at[128];
 }  // namespace
+
+WsHeader* linear_device_status(int dev) { return g_device_status_at[dev & 127]; }
 
 cudaError_t linear_init_attributes() {
   for (int b = 2; b <= 8; ++b) {
@@ -161,6 +166,9 @@ cudaError_t linear_init_attributes() {
   cudaError_t e = cudaGetDevice(&dev);
   for (int i = 1; i <= 3 && e == cudaSuccess; ++i)
     e = linear_tc_clusters<4>(1 << i, &g_clusters[dev & 127][i]);
+  void* at = nullptr;
+  if (e == cudaSuccess) e = cudaGetSymbolAddress(&at, g_device_status);
+  if (e == cudaSuccess) g_device_status_at[dev & 127] = static_cast<WsHeader*>(at);
   return e;
 }
 
@@ -243,6 +251,7 @@ cudaError_t launch_linear(const LinearArgs& a, LinearInput kind, void* ws, cudaS
   // waves, 24 us where clusters of four take 17.)
   int dev = 0, S = 1;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  t.device_hdr = linear_device_status(dev);
   for (int i = 1; !pair && i <= 3; ++i)
     if (tiles <= g_clusters[dev & 127][i] && t.stages >= 8 << i) S = 1 << i;
   CUtensorMap map;

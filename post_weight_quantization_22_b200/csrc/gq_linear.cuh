@@ -19,6 +19,7 @@ struct LinTcArgs {
   int dmask;         // 16-column steps per accumulator period (a power of two) - 1
   int groups;        // groups of a row
   WsHeader* hdr;
+  WsHeader* device_hdr;  // the device's own status: kept until it is looked at
   WaitTest wait;     // budget of the kernel's waits (test setting)
 };
 

@@ -592,7 +592,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         arrive(t_empty_at + 8 * (pt & 1));
       }
       if (!ok) {
-        if (lane == 0) record_status(a.hdr, GQ_ERR_TIMEOUT);
+        if (lane == 0) {
+          record_status(a.hdr, GQ_ERR_TIMEOUT);
+          record_status(a.device_hdr, GQ_ERR_TIMEOUT);
+        }
       } else if (kPair || S == 1) {
         const int cnt = (int)min((int64_t)(N / 2), a.l.T - tk);
         const int rows = (int)min((int64_t)32, a.l.m - row0);

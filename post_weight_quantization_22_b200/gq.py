@@ -92,6 +92,8 @@ def _load():
     lib.gq_linear_quantized_workspace_size.argtypes = [I64, I64, I64, I]
     lib.gq_linear_quantized.restype = I
     lib.gq_linear_quantized.argtypes = [P, P, I64, I64, I64, P, P, P, I, I, P, P, I, P, SZ, P]
+    lib.gq_linear_status.restype = I
+    lib.gq_linear_status.argtypes = [P]
     lib.gq_rmsnorm_quantize.restype = I
     lib.gq_rmsnorm_quantize.argtypes = [P, P, I, P, I, I64, I64, D, P, P, P, P, P]
     lib.gq_debug_wait_test.restype = I
@@ -110,7 +112,8 @@ EXPORTED = ("gq_version", "gq_status_string", "gq_hessian_accumulate", "gq_hessi
             "gq_huffman_encode", "gq_debug_wait_test", "gq_kernel_launches",
             "gq_ssqr_workspace_size", "gq_ssqr_quantize_layer", "gq_hptq_workspace_size",
             "gq_hptq_quantize_layer", "gq_order_codes", "gq_linear_workspace_size", "gq_linear",
-            "gq_linear_quantized_workspace_size", "gq_linear_quantized", "gq_rmsnorm_quantize")
+            "gq_linear_quantized_workspace_size", "gq_linear_quantized", "gq_linear_status",
+            "gq_rmsnorm_quantize")
 
 
 def _ptr(t):
@@ -567,6 +570,19 @@ def gq_linear_quantized(q: torch.Tensor, qscale: torch.Tensor, codes: torch.Tens
         y.data_ptr(), yc, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
         _raw_stream(device)), "gq_linear_quantized")
     return y
+
+
+def gq_linear_status(device=None, stream=None) -> int:
+    """The status of every gq_linear and gq_linear_quantized call that ``device`` (default: the
+    current one) finished since the last look: 0, or GQ_ERR_TIMEOUT (5) where a bounded wait ran
+    out and a y is undefined.  Synchronizes ``stream`` (default: the device's current stream)."""
+    index = torch.cuda.current_device() if device is None else torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    if _elsewhere(index, stream):
+        with on_stream(index, stream):
+            return gq_linear_status(index)
+    return int(LIB.gq_linear_status(_raw_stream(index)))
 
 
 def gq_rmsnorm_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residual=None,

@@ -67,6 +67,11 @@ class QuantizedLinear:
                                      self.group_size, self.perm, y, y_dtype or torch.bfloat16,
                                      ws, stream)
 
+    def status(self, stream=None) -> int:
+        """The status of every product on this layer's device since the last look (0, or 5 where a
+        bounded wait ran out and an output is undefined); synchronizes ``stream``."""
+        return G.gq_linear_status(self.codes.get_device(), stream)
+
 
 @dataclass
 class LayerResult:
@@ -146,7 +151,8 @@ class LayerQuantizer:
 
     def output(self, X: torch.Tensor, y=None, stream=None) -> torch.Tensor:
         """X W^T with the quantized weights, in X's type: the calibration input of what follows
-        this layer, as the quantized model will produce it."""
+        this layer, as the quantized model will produce it.  (``gq.gq_linear_status`` says whether
+        the products of a device have all come to their end.)"""
         return self.linear(stream)(X, y=y, stream=stream)
 
     def status(self):
@@ -324,8 +330,9 @@ class BlockQuantizer:
         return {name: self.out[name] for name in names}
 
     def status(self):
-        """Worst device status over every workspace (0 if all are clean); synchronizes."""
-        codes = []
+        """Worst device status over every workspace, and over the products that ``forward`` runs
+        (every product of the device since the last look); 0 if all are clean; synchronizes."""
+        codes = [G.gq_linear_status(o["codes"].get_device()) for o in list(self.out.values())[:1]]
         for d in self.inputs.values():
             codes.append(G.gq_workspace_status(d["ws_prep"])[0])
         for ws in self._ws_quant.values():

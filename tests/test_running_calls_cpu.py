@@ -103,3 +103,23 @@ def test_a_kept_ordered_layer_is_a_copy(calls):
     lq = _ordered_quantizer(group=0)
     layer = lq.linear()
     assert layer.perm is None and layer.codes is lq.codes and layer.scales is lq.scales
+
+
+def test_status_of_the_products_is_reachable(monkeypatch):
+    """QuantizedLinear.status and BlockQuantizer.status report the device's products."""
+    from post_weight_quantization_22_b200 import gq as G
+    from post_weight_quantization_22_b200.pipeline import BlockQuantizer
+    assert "gq_linear_status" in G.EXPORTED
+    asked = []
+
+    def linear_status(device=None, stream=None):
+        asked.append((device, stream))
+        return 5
+
+    monkeypatch.setattr(G, "gq_linear_status", linear_status)
+    monkeypatch.setattr(G, "gq_workspace_status", lambda ws, stream=None: (0, 0))
+    stream = object()
+    assert _ordered_quantizer(order=None).linear().status(stream) == 5
+    assert asked == [(-1, stream)]
+    bq = BlockQuantizer((("q", 8, 64, "attn"),), G.QuantCfg(bits=4), device="cpu", max_tokens=16)
+    assert bq.status() == 5

@@ -149,8 +149,43 @@ def test_a_wait_of_the_product_runs_out(form, T, m, n, dtype):
         G.gq_debug_wait_test()
     print(f"{form}: {elapsed:.3f} s")
     assert G.gq_workspace_status(ws)[0] == 5           # GQ_ERR_TIMEOUT
+    assert G.gq_linear_status() == 5 and G.gq_linear_status() == 0
     assert elapsed < 30.0
     G.gq_linear(x, *dev, bits, group, y=y, ws=ws)
-    assert G.gq_workspace_status(ws)[0] == 0
+    assert G.gq_workspace_status(ws)[0] == 0 and G.gq_linear_status() == 0
     rows = np.r_[0:8, T - 8:T]
     check_linear(y[rows], x.double().cpu().numpy()[rows], w)
+
+
+def test_a_timeout_is_seen_without_a_workspace():
+    """Calls that bring no workspace of their own, through the pipeline's objects and in a replayed
+    graph: the device's status tells of a wait that ran out, once."""
+    from post_weight_quantization_22_b200 import gq as G
+    from post_weight_quantization_22_b200.pipeline import BlockQuantizer
+    m, n, T = 4096, 256, 64
+    bq = BlockQuantizer((("q", m, n, "attn"),), G.QuantCfg(bits=4, group_size=64))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    W = (0.02 * torch.randn(m, n, generator=g, device="cuda")).bfloat16()
+    bq.run({"q": W}, {"attn": torch.randn(400, n, generator=g, device="cuda").bfloat16()})
+    layer = bq.linear("q")
+    x = torch.randn(T, n, generator=g, device="cuda").bfloat16()
+    gamma = torch.ones(n, device="cuda")
+    G.gq_linear_status()                               # what ran before
+    first = layer(x)
+    assert layer.status() == 0 and bq.status() == 0
+    graph = torch.cuda.CUDAGraph()
+    G.gq_debug_wait_test(16384, True)
+    try:
+        layer(x)
+        assert layer.status() == 5                     # GQ_ERR_TIMEOUT
+        bq.forward("attn", x, gamma)
+        assert bq.status() == 5
+        with torch.cuda.graph(graph):
+            layer(x)
+    finally:
+        G.gq_debug_wait_test()
+    assert layer.status() == 0
+    graph.replay()
+    assert G.gq_linear_status() == 5
+    side = torch.cuda.Stream()
+    assert torch.equal(layer(x), first) and layer.status() == 0 and layer.status(side) == 0
