@@ -460,6 +460,16 @@ def _need_on(t, dtype, shape, device, name):
                          f"{t.device} {t.dtype} {tuple(t.shape)}")
 
 
+def _ws_args(ws, device):
+    """A workspace's pointer and bytes."""
+    if ws is None:
+        return None, 0
+    if ws.dtype is not torch.uint8 or ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected contiguous cuda:{device} torch.uint8 (workspace), got "
+                         f"{ws.device} {ws.dtype}")
+    return ws.data_ptr(), ws.numel()
+
+
 def _rows(x, name):
     device = x.get_device()
     if x.dim() != 2 or device < 0 or not x.is_contiguous():
@@ -539,8 +549,7 @@ def gq_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros:
     _check(LIB.gq_linear(x.data_ptr(), xc, T, m, n, codes.data_ptr(), scales.data_ptr(),
                          zeros.data_ptr(), bits, group_size,
                          None if perm is None else perm.data_ptr(), y.data_ptr(), yc,
-                         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                         _raw_stream(device)), "gq_linear")
+                         *_ws_args(ws, device), _raw_stream(device)), "gq_linear")
     return y
 
 
@@ -567,8 +576,7 @@ def gq_linear_quantized(q: torch.Tensor, qscale: torch.Tensor, codes: torch.Tens
     _check(LIB.gq_linear_quantized(
         q.data_ptr(), qscale.data_ptr(), T, m, n, codes.data_ptr(), scales.data_ptr(),
         zeros.data_ptr(), bits, group_size, None if perm is None else perm.data_ptr(),
-        y.data_ptr(), yc, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-        _raw_stream(device)), "gq_linear_quantized")
+        y.data_ptr(), yc, *_ws_args(ws, device), _raw_stream(device)), "gq_linear_quantized")
     return y
 
 

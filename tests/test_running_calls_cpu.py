@@ -123,3 +123,31 @@ def test_status_of_the_products_is_reachable(monkeypatch):
     assert asked == [(-1, stream)]
     bq = BlockQuantizer((("q", 8, 64, "attn"),), G.QuantCfg(bits=4), device="cpu", max_tokens=16)
     assert bq.status() == 5
+
+
+def test_a_workspace_of_another_kind_is_refused(monkeypatch):
+    """A workspace in host memory, or one whose bytes its length does not say, never reaches the
+    library."""
+    from post_weight_quantization_22_b200 import gq as G
+    x, q = torch.zeros(64, 16), torch.zeros(64, 16, dtype=torch.int8)
+    layer = (torch.zeros(4096, 2, dtype=torch.int32), torch.ones(4096, 1),
+             torch.zeros(4096, 1, dtype=torch.uint8))
+    # tensors that say of themselves that they are on a GPU, and a library that must not be called
+    monkeypatch.setattr(G, "_rows", lambda t, name: (t.shape, 0))
+    monkeypatch.setattr(G, "_need_on", lambda *a: None)
+    monkeypatch.setattr(G, "_elsewhere", lambda *a: False)
+    monkeypatch.setattr(G, "_raw_stream", lambda device: 0)
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*a):
+                raise AssertionError(f"{name} was called")
+            return call
+
+    monkeypatch.setattr(G, "LIB", Library())
+    for ws in (torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(1 << 20),
+               torch.zeros(1, dtype=torch.uint8).expand(1 << 20)):
+        with pytest.raises(ValueError, match="ws"):
+            G.gq_linear(x, *layer, 4, y=torch.zeros(64, 4096), ws=ws)
+        with pytest.raises(ValueError, match="ws"):
+            G.gq_linear_quantized(q, torch.ones(64), *layer, 4, y=torch.zeros(64, 4096), ws=ws)

@@ -189,3 +189,16 @@ def test_a_timeout_is_seen_without_a_workspace():
     assert G.gq_linear_status() == 5
     side = torch.cuda.Stream()
     assert torch.equal(layer(x), first) and layer.status() == 0 and layer.status(side) == 0
+
+
+def test_workspace_arguments_are_checked():
+    from post_weight_quantization_22_b200 import gq as G
+    c, s, z, _ = layer_np(4096, 128, 4, 64, 2)
+    dev = to_cuda(c, s, z, 4)
+    x = torch.zeros(64, 128, device="cuda")
+    need = G.gq_linear_workspace_size(64, 4096, 128, torch.float32)
+    for ws in (torch.zeros(need, dtype=torch.uint8), torch.zeros(need, device="cuda"),
+               torch.zeros(1, dtype=torch.uint8, device="cuda").expand(need)):
+        with pytest.raises(ValueError):
+            G.gq_linear(x, *dev, 4, 64, ws=ws)
+    G.gq_linear(x, *dev, 4, 64, ws=torch.zeros(2, need, dtype=torch.uint8, device="cuda")[1])
