@@ -240,6 +240,9 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 256, V <= 2 ? 3 : V == 4 ? 2 : 
     // 127 / max|u| in fp32 where fp32 holds both; elsewhere every code is decided in fp64
     const bool quick = topd >= 0x1p-100 && topd < 0x1p120;
     const float inv = quick ? __fdividef(127.f, (float)topd) : 0.f, rstd32 = (float)rstd;
+    // y = u rstd in fp32 where rstd is a normal fp32 number and what u may have lost below fp32's
+    // normal range, 2^-150, stays below a quarter of y's smallest step; else in fp64
+    const bool quick_y = quick && rstd >= 0x1p-100 && rstd <= 0x1p15;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       Vec8<Gm> g;
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 256, V <= 2 ? 3 : V == 4 ? 2 : 
         Vec8<X> yv;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          if (kExact32 && quick) yv.v[e] = from_f32<X>(u_of(e) * rstd32);
+          if (kExact32 && quick_y) yv.v[e] = from_f32<X>(u_of(e) * rstd32);
           else yv.v[e] = from_f32<X>((float)((double)to_f32(h[k].v[e]) * (double)gam(e) * rstd));
         }
         store8<kVec>(static_cast<X*>(a.y) + row * n, first(k), step, n, yv);

@@ -202,3 +202,33 @@ def test_workspace_arguments_are_checked():
         with pytest.raises(ValueError):
             G.gq_linear(x, *dev, 4, 64, ws=ws)
     G.gq_linear(x, *dev, 4, 64, ws=torch.zeros(2, need, dtype=torch.uint8, device="cuda")[1])
+
+
+def test_norm_rows_far_below_one():
+    """bf16 rows whose 1 / rms leaves fp32, and products h gamma below fp32's normal range in rows
+    that eps does not hold down: y is the formula's, rounded once."""
+    from post_weight_quantization_22_b200 import gq as G
+    n = 256
+    g = torch.Generator(device="cuda").manual_seed(0)
+    base = torch.randn(n, generator=g, device="cuda").clamp(-3, 3)
+    odd = torch.arange(n, device="cuda") % 2 == 1
+    x = torch.stack([(base.double() * 2.0 ** e).float() for e in (-131, -120, -126, -95, -60, 0, 100)]).bfloat16()
+    gammas = []
+    gammas.append(torch.full((n,), 2.0 ** 40, device="cuda"))               # max|u| near 2^-80
+    gammas.append(torch.where(odd, 1 + 2.0 ** -7, 2.0 ** -50 * (1 + 2.0 ** -6)))
+    gammas.append(1 + 0.1 * torch.randn(n, generator=g, device="cuda"))
+    for gamma in gammas:
+        gamma = gamma.bfloat16()
+        for eps in (0.0, 1e-6):
+            r = G.gq_rmsnorm_quantize(x, gamma, eps, y=torch.empty_like(x),
+                                      q=torch.empty(len(x), n, dtype=torch.int8, device="cuda"),
+                                      qscale=torch.empty(len(x), device="cuda"))
+            h, v, q, s = norm_np(x.double().cpu().numpy(), None, gamma.double().cpu().numpy(), eps,
+                                 torch.bfloat16)
+            # half a step of bf16 relative to the value and 2^-23 for roundings in fp32 on the way;
+            # below the normal range half of the smallest step, 2^-133, and a quarter for the way
+            half = torch.finfo(torch.bfloat16).eps / 2 + 2.0 ** -23
+            got = r["y"].double().cpu().numpy()
+            off = np.abs(got - v) - (half * np.abs(v) + 0.75 * 2.0 ** -133)
+            assert np.all(off <= 0), (eps, np.argwhere(~(off <= 0))[:4], float(off.max()))
+            assert np.array_equal(r["q"].cpu().numpy().astype(int), q)
