@@ -407,12 +407,16 @@ size_t gq_linear_workspace_size(int64_t T, int64_t m, int64_t n, gq_dtype x_dtyp
 /*
  * y = x W^T with the packed layer W:
  *   y[t][r] = sum over groups g of scale[r][g] * sum over k in g of x[t][k] (code[r][k] - zero[r][g]).
- * Products of x and code - zero are exact (fp32 x as three bf16 parts that add up to it), summed
- * in fp32 inside a group, scaled and added up in fp32; y is rounded once.  A token's result does
- * not depend on the other tokens' values, and no sum depends on timing: equal calls give equal
- * bits.
+ * Products of x and code - zero are exact (fp32 x as three bf16 parts that add up to it; of a
+ * value below 2^-110 what lies below 2^-133 is dropped), summed in fp32 inside a group, scaled and
+ * added up in fp32; y is rounded once.  The sums inside a group are the tensor cores', which
+ * truncate (2^-23 a step) and whose range is fp32's: a sum of x (code - zero) beyond it is infinite
+ * whatever the scale.  A token's result does not depend on the other tokens' values, and no sum
+ * depends on timing: equal calls give equal bits.
  *
- *   d_x       T x n, bf16 or fp32 (any alignment of the element type).
+ *   d_x       T x n, bf16 or fp32 (any alignment of the element type; many bf16 tokens off a
+ *             16-byte boundary take the kernel for few tokens: through 4096 x 4096, 64 tokens 6
+ *             times slower, 4096 tokens 50 times).
  *   d_codes   m x ceil(n*b/32) uint32; d_scales m x G fp32; d_zeros m x G uint8 with values in
  *             [0, 2^b - 1], G = 1 (group_size 0) or ceil(n / group_size).
  *   bits      2..8.   group_size  0, 16, 32, 64 or 128.
@@ -459,8 +463,10 @@ gq_status gq_linear_status(gq_stream_t stream);
  *   rstd = 1 / sqrt(mean(h^2) + eps),   d_y = h gamma rstd,
  *   d_q = rint(127 u / max|u|) with u = h gamma (half to even; 0 in a row of zeros),
  *   d_qscale = max|u| rstd / 127, so that d_qscale d_q stands for h gamma rstd.
- * Statistics and the decision of every code are in fp64.  A row with an infinity or a NaN in it
- * gets the scale NaN and codes 0; other rows are not affected.
+ * Statistics and the decision of every code are in fp64; with bf16 x and gamma, d_y is rounded from
+ * fp32 (2^-23 before its own rounding).  A row with an infinity or a NaN in it gets the scale NaN and
+ * codes 0; other rows are not affected.  With eps = 0 a row of zeros is 0 / 0: its scale and its
+ * d_y are NaN, its codes 0 (with eps > 0 all three are 0).
  *
  *   d_x         T x n, bf16 or fp32.   d_residual  T x n of the same type, or NULL (h = x).
  *   d_gamma     n, bf16 or fp32 (gamma_dtype).   eps >= 0, finite.

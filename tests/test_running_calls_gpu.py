@@ -232,3 +232,23 @@ def test_norm_rows_far_below_one():
             off = np.abs(got - v) - (half * np.abs(v) + 0.75 * 2.0 ** -133)
             assert np.all(off <= 0), (eps, np.argwhere(~(off <= 0))[:4], float(off.max()))
             assert np.array_equal(r["q"].cpu().numpy().astype(int), q)
+
+
+@pytest.mark.parametrize("dtype", (torch.bfloat16, torch.float32))
+def test_norm_of_a_row_of_zeros(dtype):
+    """With eps > 0 everything is 0; without it the row is 0 / 0, and says so."""
+    from post_weight_quantization_22_b200 import gq as G
+    n = 300
+    x = torch.zeros(3, n, dtype=dtype, device="cuda")
+    x[1] = 1
+    gamma = torch.ones(n, dtype=dtype, device="cuda")
+    for eps in (1e-6, 0.0):
+        r = G.gq_rmsnorm_quantize(x, gamma, eps, y=torch.empty_like(x),
+                                  q=torch.full((3, n), 9, dtype=torch.int8, device="cuda"),
+                                  qscale=torch.empty(3, device="cuda"))
+        assert not r["q"][::2].any() and bool((r["q"][1] == 127).all())
+        want = 0.0 if eps else float("nan")
+        for t in (r["y"][::2], r["qscale"][::2]):
+            assert torch.equal(t.isnan(), torch.full_like(t, want).isnan())
+            assert eps == 0 or not t.any()
+        assert bool(r["y"][1].isfinite().all()) and bool(r["qscale"][1].isfinite())
