@@ -13,7 +13,8 @@
 // c - z is an exact integer in 16 bits, the products are exact, and the fp32 sums of one group
 // are multiplied by the group's scale in fp32: no weight is rounded.  The warps of a CTA share
 // the columns in chunks of 128 and add their sums in a fixed order; every warp loads a chunk
-// ahead.
+// ahead.  What holds it is latency at its occupancy, with no pipe full (one token, 32768 x 8192, 4
+// bits: ALU 47 %, issue 49 %, DRAM 34 %, 24 % of the warps active): the chunk ahead is registers.
 //
 // fp32 tokens are taken as three bf16 parts (8 + 8 + 8 bits, exact), three products a weight;
 // 8-bit tokens as fp16 integers.

@@ -7,6 +7,8 @@
 //
 // The bound is the traffic: a row is read once, kept in registers and written once; what is done
 // per value has to stay below about 40 issue cycles of a warp for that (bf16, 7 bytes a value).
+// (8192 x 4096 bf16 with a residual: 59 us against 36 of the traffic; a block's next loads wait for
+// its row's stores.)
 // h^2 is summed in fp64: the square of any value is in range, and one conversion and one addition
 // per value run on pipes of their own.  u = h gamma is exact in fp32 for bf16 inputs and weights,
 // in fp64 otherwise.  A code is first taken from the fp32 quotient, which is within 3e-5 of the
